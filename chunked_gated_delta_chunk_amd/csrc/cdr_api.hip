@@ -343,7 +343,7 @@ const char* cdr_status_str(cdr_status s) {
         case CDR_OK: return "ok";
         case CDR_ERR_NULL_ARG: return "a required pointer is NULL";
         case CDR_ERR_BAD_SHAPE: return "non-positive or inconsistent sizes";
-        case CDR_ERR_UNSUPPORTED: return "unsupported configuration (K and V must be 128, chunk_size 64 or 128)";
+        case CDR_ERR_UNSUPPORTED: return "unsupported configuration (K and V must be 128, chunk_size 64 or 128; or a type, activation or width the entry point does not take)";
         case CDR_ERR_VARLEN_BATCH: return "cu_seqlens requires B == 1";
         case CDR_ERR_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
         case CDR_ERR_HIP: return "HIP kernel launch failed";

@@ -24,8 +24,10 @@ EXPORTED = ("cdr_check", "cdr_workspace_bytes", "chunk_dr_fwd", "chunk_dr_fwd_st
             "chunk_dr_fwd_noalloc",
             "cdr_bwd_workspace_bytes", "chunk_dr_bwd", "chunk_dr_bwd_stages",
             "chunk_dr_segment_map", "chunk_dr_merge_states",
-            "cdr_recurrent_check", "chunk_dr_recurrent_fwd", "cdr_check_cu_seqlens", "cdr_status_str",
-            "cdr_version")
+            "cdr_recurrent_check", "chunk_dr_recurrent_fwd", "cdr_check_cu_seqlens",
+            "cdr_block_norm_check", "cdr_block_norm_fwd", "cdr_block_norm_bwd_workspace_bytes",
+            "cdr_block_norm_bwd", "cdr_page_tables_workspace_bytes", "cdr_build_page_tables",
+            "cdr_status_str", "cdr_version")
 STATE_SEPARATE, STATE_POOL, STATE_POOL_SPEC = 0, 1, 2
 STAGE_INTRA, STAGE_CHAIN, STAGE_OUTPUT, STAGE_ALL = 1, 2, 4, 7
 NOALLOC_SCRATCH_BYTES = 256 * 1024 * 1024   # CDR_NOALLOC_SCRATCH_BYTES of chunk_dr.h
@@ -49,6 +51,16 @@ class cdr_recurrent_problem(ctypes.Structure):
                 ("state_mode", ctypes.c_int32), ("has_initial_state", ctypes.c_int32),
                 ("output_final_state", ctypes.c_int32), ("num_slots", ctypes.c_int32),
                 ("index_cols", ctypes.c_int32)]
+
+
+class cdr_block_norm_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("gate_act", ctypes.c_int32),
+                ("has_weight", ctypes.c_int32), ("has_residual", ctypes.c_int32),
+                ("has_scale", ctypes.c_int32), ("has_next", ctypes.c_int32),
+                ("inner", ctypes.c_int32), ("alpha", ctypes.c_float), ("eps", ctypes.c_float),
+                ("y_stride", ctypes.c_int64 * 2), ("gate_stride", ctypes.c_int64 * 2),
+                ("residual_stride", ctypes.c_int64 * 2)]
 
 
 _lib = None
@@ -93,6 +105,19 @@ def load_library(path: str = LIB_PATH):
     lib.chunk_dr_recurrent_fwd.restype = ctypes.c_int
     lib.cdr_check_cu_seqlens.argtypes = [vp, ctypes.c_int32, ctypes.c_int32, vp, vp]
     lib.cdr_check_cu_seqlens.restype = ctypes.c_int
+    NP = ctypes.POINTER(cdr_block_norm_problem)
+    lib.cdr_block_norm_check.argtypes = [NP]
+    lib.cdr_block_norm_check.restype = ctypes.c_int
+    lib.cdr_block_norm_fwd.argtypes = [NP] + [vp] * 9
+    lib.cdr_block_norm_fwd.restype = ctypes.c_int
+    lib.cdr_block_norm_bwd_workspace_bytes.argtypes = [NP]
+    lib.cdr_block_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.cdr_block_norm_bwd.argtypes = [NP] + [vp] * 15 + [ctypes.c_size_t, vp]
+    lib.cdr_block_norm_bwd.restype = ctypes.c_int
+    lib.cdr_page_tables_workspace_bytes.argtypes = [ctypes.c_int32]
+    lib.cdr_page_tables_workspace_bytes.restype = ctypes.c_size_t
+    lib.cdr_build_page_tables.argtypes = [ctypes.c_int32] * 5 + [vp] * 12 + [ctypes.c_size_t, vp]
+    lib.cdr_build_page_tables.restype = ctypes.c_int
     lib.cdr_status_str.argtypes = [ctypes.c_int]
     lib.cdr_status_str.restype = ctypes.c_char_p
     lib.cdr_version.argtypes = []

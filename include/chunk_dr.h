@@ -33,6 +33,10 @@
  *    to the host or synchronises; kernels are queued on the given stream and the
  *    call returns immediately.
  *  - Errors are returned as cdr_status values; nothing is printed or thrown.
+ *
+ * Beside the operator stand the parts of a block and of a serving step that touch it: the norms,
+ * gate and residual at a block's boundary (cdr_block_norm_*), and the offsets, page tables and
+ * slots of a step from its request lengths (cdr_build_page_tables).
  */
 #ifndef CHUNK_DR_H
 #define CHUNK_DR_H
@@ -44,13 +48,14 @@
 extern "C" {
 #endif
 
-#define CDR_VERSION 8
+#define CDR_VERSION 9
 
 typedef enum {
     CDR_OK = 0,
     CDR_ERR_NULL_ARG = 1,      /* a required pointer is NULL */
     CDR_ERR_BAD_SHAPE = 2,     /* non-positive or inconsistent sizes */
-    CDR_ERR_UNSUPPORTED = 3,   /* K or V != 128, chunk_size not 64 or 128, unknown gate */
+    CDR_ERR_UNSUPPORTED = 3,   /* K or V != 128, chunk_size not 64 or 128, unknown gate, type or
+                                  activation, a width the entry point does not take */
     CDR_ERR_VARLEN_BATCH = 4,  /* cu_seqlens given with B != 1 */
     CDR_ERR_WORKSPACE = 5,     /* workspace NULL or smaller than cdr_workspace_bytes() */
     CDR_ERR_HIP = 6,           /* a kernel launch failed (hipGetLastError) */
@@ -389,6 +394,133 @@ cdr_status chunk_dr_recurrent_fwd(const cdr_recurrent_problem* p,
                                   float* state_pool, const int32_t* ssm_state_indices,
                                   const int32_t* num_accepted_tokens,
                                   void* o, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The block boundary: the norm after a token mixer, its gate, the residual and the norm before the
+ * next block, in one pass over the data.  For every row (a token, or a token and head), with
+ * rstd(x) = 1 / sqrt(mean x^2 + eps) over the row's D elements:
+ *
+ *     n = y * rstd(y) * weight                      (has_weight; else n = y)
+ *     r = residual + alpha * res_scale * a(gate) * n
+ *                                                   a(z) = sigmoid(z) or z * sigmoid(z); residual,
+ *                                                   res_scale and gate each optional
+ *     h = r * rstd(r) * next_weight                 (has_next)
+ *
+ * `out` receives r and `next_out` h.  Arithmetic is fp32 whatever the types; h is formed from the
+ * fp32 r and each output is rounded once.  With D = 128, a gate, a weight and nothing else this is
+ * the gated norm of o [.., HV, V] per head; with everything it is a whole block boundary.
+ *
+ *   y, gate      dtype, rows of D contiguous elements (strides below)
+ *   residual     res_dtype, likewise
+ *   weight, res_scale, next_weight   fp32 [D]
+ *   out          res_dtype with a residual, else dtype; dense [rows, D]
+ *   next_out     dtype, dense [rows, D]
+ * out may be residual itself, and next_out y itself, when those are dense (every element is read
+ * before it is written, by the same thread); any other overlap of inputs and outputs is undefined.
+ *
+ * Strides: row i of an operand starts at element (i / inner) * stride[0] + (i % inner) * stride[1]
+ * (inner 0 or 1: i * stride[0]), so a slice [T, HV, 128] of a wider projection is read in place.
+ * D is 1 to 8192.  Rows of 16-byte aligned operands with D and strides divisible by 8 are read and
+ * written 16 bytes at a time, others element by element.
+ * ------------------------------------------------------------------------------------------ */
+typedef enum {
+    CDR_BF16 = 0,
+    CDR_F32 = 1
+} cdr_dtype;
+
+typedef enum {
+    CDR_ACT_NONE = 0,          /* no gate */
+    CDR_ACT_SIGMOID = 1,
+    CDR_ACT_SILU = 2
+} cdr_act;
+
+typedef struct {
+    int32_t rows;
+    int32_t D;
+    int32_t dtype;              /* cdr_dtype of y, gate, next_out and their gradients */
+    int32_t res_dtype;          /* cdr_dtype of residual, out and their gradients (has_residual) */
+    int32_t gate_act;           /* cdr_act */
+    int32_t has_weight;
+    int32_t has_residual;
+    int32_t has_scale;
+    int32_t has_next;
+    int32_t inner;              /* rows of one outer step, a divisor of rows; 0 means 1 */
+    float alpha;
+    float eps;                  /* >= 0 */
+    int64_t y_stride[2];        /* elements: outer, inner */
+    int64_t gate_stride[2];
+    int64_t residual_stride[2];
+} cdr_block_norm_problem;
+
+/* Host-only validation of a block norm problem. */
+cdr_status cdr_block_norm_check(const cdr_block_norm_problem* p);
+
+/* One kernel on `stream`; nothing for rows == 0.  Pointers whose flag is 0 may be NULL. */
+cdr_status cdr_block_norm_fwd(const cdr_block_norm_problem* p, const void* y, const void* gate, const void* residual,
+                              const float* weight, const float* res_scale, const float* next_weight, void* out,
+                              void* next_out, void* stream);
+
+/*
+ * Gradients of L = sum(out * d_out) + sum(next_out * d_next).  Inputs as the forward, which is
+ * recomputed (nothing is kept from it).
+ *
+ *   d_out    type of out, dense; NULL means zero, allowed with has_next
+ *   d_next   dtype, dense (has_next)
+ *   dy, dgate (dtype), dresidual (res_dtype)      dense [rows, D], written where their input is given
+ *   dweight, dres_scale, dnext_weight             fp32 [D], sums over the rows (zeros for rows == 0)
+ *   workspace  at least cdr_block_norm_bwd_workspace_bytes(p) bytes, 16-byte aligned, contents
+ *              irrelevant, not to be used by another call until this one's kernels have finished
+ * No output may overlap an input.  Column sums are added in a fixed order: repeated calls give the
+ * same bits.
+ */
+size_t cdr_block_norm_bwd_workspace_bytes(const cdr_block_norm_problem* p);
+
+cdr_status cdr_block_norm_bwd(const cdr_block_norm_problem* p, const void* y, const void* gate, const void* residual,
+                              const float* weight, const float* res_scale, const float* next_weight, const void* d_out,
+                              const void* d_next, void* dy, void* dgate, void* dresidual, float* dweight,
+                              float* dres_scale, float* dnext_weight, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Bookkeeping of a serving step on the device, from the lengths of its requests: the offsets that
+ * the packed forward and decode take (cu_seqlens), positions, the page table and the slots of a
+ * paged cache, with new pages taken from a list of free ones.  All arrays are int32 on the device;
+ * with q_n = max(query_lens[n], 0), c_n = max(context_lens[n], 0), P = page_size, W = table_cols:
+ *
+ *     cu_seqlens[0] = 0, cu_seqlens[n + 1] = min(cu_seqlens[n] + q_n, max_tokens)
+ *     len_n   = c_n + (cu_seqlens[n + 1] - cu_seqlens[n])       -> seq_lens[n]
+ *     held_n  = min(ceil(c_n / P), W)       pages that the request holds already
+ *     upto_n  = min(ceil(len_n / P), W)     pages that it holds after the step
+ *     head    = clip(free_head[0], 0, num_free);  first_n = head + sum of (upto_m - held_m), m < n
+ *     block_table[n, held_n + j] = free_pages[first_n + j], -1 behind the list's end
+ *     free_head_out[0] = min(first_N, num_free)
+ *     shortage[0] = max(first_N - num_free, 0) + sum of (ceil(len_n / P) - upto_n)
+ *
+ * and for token t of request n (cu_seqlens[n] <= t < cu_seqlens[n + 1]), p = c_n + t - cu_seqlens[n]:
+ *
+ *     positions[t] = p,   slot_map[t] = block_table[n, p / P] * P + p % P
+ *
+ * slot_map[t] = -1 where that page is missing (p / P >= W, a negative entry, or a slot beyond
+ * int32), which the cache writers skip.  Tokens behind the last request (t >= cu_seqlens[N]) get
+ * position 0 and slot -1, so that a step padded to a captured size writes nothing for them.  Table
+ * entries other than the new pages' are left as they were.  free_pages[free_head:] is the stack of
+ * free pages: a caller gives pages back by writing them below the head and lowering it.
+ * shortage[0] counts the pages that were wanted and are not there; a step with a shortage is still
+ * well defined (no access leaves the arrays).  free_head_out may be free_head (in place).
+ *
+ *   query_lens, context_lens [N];  block_table [N, table_cols], updated in place
+ *   free_pages [num_free];  free_head, free_head_out, shortage [1]
+ *   cu_seqlens [N + 1];  seq_lens [N];  positions, slot_map [max_tokens]
+ *   workspace  at least cdr_page_tables_workspace_bytes(N) bytes
+ * One kernel is queued for up to 4096 tokens, two beyond.
+ * ------------------------------------------------------------------------------------------ */
+size_t cdr_page_tables_workspace_bytes(int32_t N);
+
+cdr_status cdr_build_page_tables(int32_t N, int32_t table_cols, int32_t num_free, int32_t page_size, int32_t max_tokens,
+                                 const int32_t* query_lens, const int32_t* context_lens, int32_t* block_table,
+                                 const int32_t* free_pages, const int32_t* free_head, int32_t* free_head_out,
+                                 int32_t* cu_seqlens, int32_t* seq_lens, int32_t* positions, int32_t* slot_map,
+                                 int32_t* shortage, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* cdr_status_str(cdr_status s);

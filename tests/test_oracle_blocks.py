@@ -1,0 +1,160 @@
+"""The oracles of the block boundary and of the page tables, on the CPU: gradients against central
+differences in fp64, tables against hand-written ones, and the binding's refusals."""
+import ctypes
+
+import pytest
+import torch
+
+import chunked_gated_delta_chunk_amd as cdr
+from chunked_gated_delta_chunk_amd import ops
+from oracle.norm import block_norm
+from oracle.pages import build_page_tables
+
+
+def _inputs(D=7, rows=3, seed=0, post=True, gate=True, res=True, scale=True, pre=True):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    return dict(y=r(rows, D), weight=r(D) if post else None, gate=r(rows, D) if gate else None,
+                residual=r(rows, D) if res else None, res_scale=r(D) if scale else None,
+                next_weight=r(D) if pre else None), r(rows, D), r(rows, D) if pre else None
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("parts", [(1, 1, 1, 1, 1), (1, 1, 0, 0, 0), (0, 0, 1, 1, 1), (1, 0, 1, 0, 1), (0, 1, 0, 1, 0)])
+def test_norm_gradients_match_differences(act, parts):
+    kw, dr, dh = _inputs(post=parts[0], gate=parts[1], res=parts[2], scale=parts[3], pre=parts[4])
+    got = block_norm(**kw, gate_act=act, d_out=dr, d_next=dh)
+
+    def loss(**k):
+        o = block_norm(**k, gate_act=act)
+        return float((o["r"][0] * dr).sum() + ((o["h"][0] * dh).sum() if dh is not None else 0))
+
+    names = dict(y="dy", weight="dweight", gate="dgate", residual="dresidual", res_scale="dres_scale",
+                 next_weight="dnext_weight")
+    step = 1e-6
+    for name, t in kw.items():
+        if t is None:
+            assert names[name] not in got
+            continue
+        flat = t.reshape(-1)
+        for i in range(0, flat.numel(), 3):
+            keep = float(flat[i])
+            flat[i] = keep + step
+            up = loss(**kw)
+            flat[i] = keep - step
+            down = loss(**kw)
+            flat[i] = keep
+            # central differences: step^2 times the third derivative, and rounding of the loss / step
+            assert abs((up - down) / (2 * step) - float(got[names[name]][0].reshape(-1)[i])) < 1e-6
+
+
+def test_norm_magnitudes_cover_the_values():
+    kw, dr, dh = _inputs()
+    for name, (value, mag) in block_norm(**kw, d_out=dr, d_next=dh).items():
+        assert (value.abs() <= mag * (1 + 1e-12)).all(), name
+
+
+def test_page_tables_by_hand():
+    # two tokens a page; request 0 holds 3 tokens (one place left), request 1 none, request 2 takes no token
+    got = build_page_tables([2, 3, 0], [3, 0, 2], [[7, 8, -1], [-1, -1, -1], [5, -1, -1]], [9, 4, 6, 1], 1, 2, 7)
+    assert got["cu_seqlens"] == [0, 2, 5, 5] and got["seq_lens"] == [5, 3, 2]
+    assert got["block_table"] == [[7, 8, 4], [6, 1, -1], [5, -1, -1]]
+    assert got["positions"] == [3, 4, 0, 1, 2, 0, 0]
+    assert got["slot_map"] == [17, 8, 12, 13, 2, -1, -1]
+    assert got["free_head"] == 4 and got["shortage"] == 0
+    # one page short, a full row, a cut at three tokens
+    got = build_page_tables([9, 2], [0, 1], [[-1, -1], [3, -1]], [5], 0, 2, 3)
+    assert got["cu_seqlens"] == [0, 3, 3] and got["block_table"] == [[5, -1], [3, -1]]
+    assert got["slot_map"] == [10, 11, -1] and got["shortage"] == 1 and got["free_head"] == 1
+
+
+# --------------------------------------------------------------------------------------- refusals
+
+def test_norm_struct_matches_header():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(ops.__file__), "..", "include", "chunk_dr.h")).read()
+    body = re.search(r"typedef struct \{([^{}]*)\} cdr_block_norm_problem;", text).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    fields = re.findall(r"(?:int32_t|int64_t|float)\s+(\w+)(?:\[2\])?;", body)
+    assert fields == [f[0] for f in ops.cdr_block_norm_problem._fields_]
+
+
+def _problem(**kw):
+    p = ops.cdr_block_norm_problem()
+    p.rows, p.D, p.alpha, p.eps = 4, 8, 1.0, 1e-6
+    for k, v in kw.items():
+        setattr(p, k, v)
+    return p
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), 0), (dict(rows=0), 0), (dict(D=8192), 0), (dict(rows=-1), 2), (dict(D=0), 2), (dict(D=8193), 3),
+    (dict(dtype=2), 3), (dict(has_residual=1, res_dtype=5), 3), (dict(gate_act=3), 3), (dict(inner=3), 2),
+    (dict(inner=2), 0), (dict(inner=-1), 2), (dict(eps=-1.0), 2), (dict(eps=float("nan")), 2),
+])
+def test_norm_check_status(kw, status):
+    assert cdr.load_library().cdr_block_norm_check(ctypes.byref(_problem(**kw))) == status
+
+
+def test_norm_rejects_missing_pointers_without_touching_device():
+    lib = cdr.load_library()
+    fake = 1 << 20
+    p = _problem(has_weight=1)
+    assert lib.cdr_block_norm_fwd(ctypes.byref(p), fake, None, None, None, None, None, fake, None, None) == 1
+    p = _problem(has_next=1)
+    assert lib.cdr_block_norm_fwd(ctypes.byref(p), fake, None, None, None, None, fake, fake, None, None) == 1
+    p = _problem()   # no gradient of r and no next norm
+    assert lib.cdr_block_norm_bwd(ctypes.byref(p), fake, *([None] * 5), None, None, fake, *([None] * 5), fake,
+                                  1 << 20, None) == 1
+    p = _problem(has_weight=1)
+    assert lib.cdr_block_norm_bwd(ctypes.byref(p), fake, None, None, fake, None, None, fake, None, fake, None, None,
+                                  fake, None, None, None, 0, None) == 5
+
+
+def test_norm_binding_errors():
+    y = torch.zeros(3, 8, dtype=torch.bfloat16)
+    w = torch.ones(8)
+    for bad, kw in ((TypeError, dict(y=y.half())), (TypeError, dict(weight=w.double())),
+                    (ValueError, dict(weight=w[:4])), (ValueError, dict(gate=y[:2])),
+                    (TypeError, dict(gate=y.float())), (ValueError, dict(gate=y, gate_act="relu")),
+                    (ValueError, dict(gate=y, gate_act=None)), (TypeError, dict(residual=y.half())),
+                    (ValueError, dict(next_out=y)), (ValueError, dict(out=y.t().contiguous().t())),
+                    (ValueError, dict())):          # host tensors: no CPU path exists
+        with pytest.raises(bad):
+            cdr.block_norm_fwd(**{"y": y, **kw})
+    with pytest.raises(ValueError, match="d_out"):
+        cdr.block_norm_bwd(y, None)
+    with pytest.raises(ValueError, match="together"):
+        cdr.block_norm_bwd(y, y, next_weight=w)
+    with pytest.raises(ValueError):
+        cdr.block_norm_fwd(torch.zeros(1, 8193))
+
+
+def test_pages_rejects_bad_arguments_without_touching_device():
+    lib = cdr.load_library()
+    fake = 1 << 20
+    ok = [2, 4, 8, 16, 32]
+    for i, v in ((0, 0), (1, 0), (2, -1), (3, 0), (4, -1)):
+        sizes = list(ok)
+        sizes[i] = v
+        assert lib.cdr_build_page_tables(*sizes, *([fake] * 12), 64, None) == 2
+    for i in range(11):
+        args = [fake] * 11
+        args[i] = None
+        assert lib.cdr_build_page_tables(*ok, *args, fake, 64, None) == 1, i
+    assert lib.cdr_build_page_tables(*ok, *([fake] * 11), fake, 4, None) == 5
+    assert lib.cdr_build_page_tables(*ok, *([fake] * 11), None, 64, None) == 5
+
+
+def test_pages_binding_errors():
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    good = dict(query_lens=i32(3), context_lens=i32(3), block_table=i32(3, 4), free_pages=i32(9), free_head=i32(1),
+                page_size=16, max_tokens=8)
+    for bad, kw in ((TypeError, dict(query_lens=i32(3).long())), (ValueError, dict(query_lens=i32(0))),
+                    (ValueError, dict(context_lens=i32(2))), (ValueError, dict(block_table=i32(4, 3).t())),
+                    (ValueError, dict(block_table=i32(2, 4))), (ValueError, dict(free_head=i32(2))),
+                    (ValueError, dict(page_size=0)), (ValueError, dict(max_tokens=-1)),
+                    (ValueError, dict(free_pages=i32(3, 3))), (ValueError, dict())):
+        with pytest.raises(bad):
+            cdr.build_page_tables(**{**good, **kw})
