@@ -1,0 +1,58 @@
+// What the latent attention kernels share (gfx950).
+#pragma once
+#include "cdr_common.h"
+
+namespace cdr {
+
+constexpr int LC = 512;             // latent dimensions of a cached key, also the values' of the absorbed form
+constexpr int LR = 64;              // rope dimensions
+constexpr int LROW = LC + LR;       // a cached key
+constexpr float LOG2E = 1.44269504088896341f;
+constexpr float LN2 = 0.69314718055994531f;
+
+typedef __attribute__((address_space(3))) char lds_char;
+
+// One 16-byte global-to-LDS copy a lane: lane l's 16 bytes at `src` go to LDS offset lds + 16 l; lds is
+// the same for the whole wave, which is whole.  Written as one block without register outputs, so
+// that the compiler neither waits for it before later LDS reads nor reuses a register of it; the
+// caller waits with dma_wait() before the barrier behind which the data is read.  m0 is written: no
+// kernel that uses it keeps anything there (gfx9 LDS instructions do not need it).
+__device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+// the same from a base shared by the wave and each lane's byte offset
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Byte offset of an LDS pointer, as m0 and the asm above take it.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// Transposing LDS read: each lane gives the address of four bf16; in each group of 16 lanes these are
+// a 4 x 16 tile (lanes 4 k .. 4 k + 3 hold row k), and lane i receives its column i, rows 0 to 3.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ s16x4 lds_tr(const void* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)(__attribute__((address_space(3))) void*)const_cast<void*>(p));
+}
+__device__ __forceinline__ bf16x8 join8(const s16x4& a, const s16x4& b) {
+    const bf16x8 r = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    return r;
+}
+__device__ __forceinline__ bf16x8 lds16(const void* p) { return *static_cast<const bf16x8*>(p); }
+
+// base-2 exponential and logarithm of the hardware (one unit in the last place)
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
+
+// A value that the compiler computes where it is used: copies of a loop's fixed offsets for every
+// unrolled step, kept in registers over the loop, cost more than the one addition that makes them.
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+}  // namespace cdr

@@ -1,0 +1,549 @@
+// Latent attention in the absorbed form, over a paged cache: the decode path.
+//
+// A cached key is one row of 576 bf16 shared by all heads: 512 latent dimensions c, which are also
+// its value, and 64 rope dimensions r.  For a new token's head, with its key limit (causal among the
+// new tokens),
+//
+//     s_j = scale (q_c . c_j + q_r . r_j),   o = sum_j softmax(s)_j c_j,   lse = log sum_j exp s_j.
+//
+// All heads (and new tokens) of a sequence read the same keys, so they are the rows of one matrix
+// product: 2 (576 + 512) flops a key and row against 1152 bytes a key.  With 16 rows the cache's
+// bytes bound it, with 128 the matrix rate is as near.
+//
+// A workgroup of four waves (eight for M = 64) takes M = 16, 32 or 64 rows and walks over tiles of
+// 64 keys.
+//  - A tile (72 KiB) goes to LDS once, two deep, by 16-byte copies that need no registers; a key's
+//    latent row is one wave's copy, so its page is looked up in scalar registers.  16-byte pieces
+//    are stored at position p ^ (key & 15), which spreads both reads below over the banks.
+//  - Scores: a wave takes 16 keys against all M rows (half of them at M = 64); the rows' q stays in
+//    registers as the right operand, so the result S^T has a row of q in each lane and the running
+//    maximum is a lane's own value after two shuffles and one exchange between the waves.
+//  - Values: a wave takes its share of the 512 columns, O^T += V^T P^T, V^T through the transposing
+//    read; P^T goes through LDS in the operand's order.  So the tile is read from LDS once or twice
+//    a product and not once for every 16 rows, which would be the bound.
+//
+// Work is cut evenly over the device whatever the lengths: the tiles of all (sequence, row block)
+// units are numbered and each workgroup takes an equal run of them.  A unit that one workgroup
+// covers is written directly; a unit cut between workgroups leaves partial sums (fp32, with their
+// maximum and sum) that a second kernel joins in order.  The cut depends on the lengths and sizes
+// alone, so the same inputs give the same bits.
+#include "chunk_dr.h"
+#include "cdr_latent.h"
+
+namespace cdr {
+
+namespace {
+
+constexpr int DEC_GRID = 256;        // workgroups; LDS holds one on a CU
+constexpr int DEC_KEYS = 64;         // keys of a tile
+
+struct LatentDecodeArgs {
+    const uint16_t* qc;
+    const uint16_t* qr;
+    const uint16_t* cache;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* cu;
+    uint16_t* o;
+    float* lse;
+    float* part;       // [2 grid][M][512] partial sums
+    float2* part_ml;   // [2 grid][M] their maximum (base 2) and sum
+    int4* rec;         // [grid] (n, row block, last workgroup) of the unit cut at this workgroup's end
+    int64_t qct, qch, qrt, qrh;
+    int N, T, H, cols, num_pages, shift;
+    float scale2;      // scale * log2(e)
+};
+
+struct SeqInfo {
+    int bos, tokens, len;    // first new token, new tokens, keys
+};
+
+__device__ __forceinline__ SeqInfo dec_seq(const LatentDecodeArgs& a, int n) {
+    SeqInfo s;
+    if (a.cu) {
+        s.bos = min(max(a.cu[n], 0), a.T);
+        s.tokens = min(max(a.cu[n + 1], s.bos), a.T) - s.bos;
+    } else {
+        s.bos = n * a.T;
+        s.tokens = a.T;
+    }
+    const int64_t room = (int64_t)a.cols << a.shift;
+    s.len = (int)min((int64_t)max(a.lens[n], 0), min(room, (int64_t)INT32_MAX - 127));   // key numbers of a whole tile stay in int
+    return s;
+}
+
+// key tiles of a sequence, at least one so that rows without keys are written too
+__device__ __forceinline__ int dec_tiles(const SeqInfo& s) { return max((s.len + DEC_KEYS - 1) / DEC_KEYS, 1); }
+
+template <int M>
+__device__ __forceinline__ int dec_blocks(const SeqInfo& s, int H) {
+    return (int)(((int64_t)s.tokens * H + M - 1) / M);
+}
+
+// Cache row of key `key` of sequence n, or -1 where there is none.
+__device__ __forceinline__ int dec_row(const LatentDecodeArgs& a, int n, int len, int key) {
+    if (key >= len) return -1;
+    const int page = a.table[(size_t)n * a.cols + (key >> a.shift)];
+    if (page < 0 || page >= a.num_pages) return -1;
+    return (page << a.shift) + (key & ((1 << a.shift) - 1));
+}
+
+template <int MT, int NW>
+__global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeArgs a) {
+    constexpr int M = 16 * MT;
+    constexpr int RH = NW / 4, MQ = MT / RH;   // row parts of the scores, row tiles of a wave there
+    constexpr int CT = 32 / NW;                // 16-column tiles of a wave in the values' product
+    constexpr int KPW = DEC_KEYS / NW;         // keys of a tile that a wave copies
+    constexpr int DEC_THREADS = 64 * NW;
+    __shared__ __align__(256) char kc[2][DEC_KEYS * LC * 2];
+    __shared__ __align__(256) char kr[2][DEC_KEYS * LR * 2];
+    __shared__ __align__(16) char pf[MT * 2 * 1024];   // P^T in operand order
+    __shared__ float mx[4][M];
+    __shared__ int64_t scan[NW];
+    __shared__ int64_t found[2];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, q = lane >> 4;
+    const int kg = w & 3, rh = w >> 2;         // the wave's keys and row part in the scores
+    const int wg = blockIdx.x;
+
+    // total tiles, then the sequence in which this workgroup's run begins
+    int64_t total = 0;
+    for (int n = tid; n < a.N; n += DEC_THREADS) {
+        const SeqInfo s = dec_seq(a, n);
+        total += (int64_t)dec_blocks<M>(s, a.H) * dec_tiles(s);
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) total += __shfl_xor(total, m, 64);
+    if (lane == 0) scan[w] = total;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) total += scan[i];
+    __syncthreads();
+    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t begin = wg * share, end = min(total, begin + share);
+    if (tid == 0) a.rec[wg] = make_int4(-1, 0, 0, 0);
+    if (begin >= end) return;
+    int64_t before = 0;
+    for (int base = 0; base < a.N; base += DEC_THREADS) {
+        const int n = base + tid;
+        int64_t own = 0;
+        if (n < a.N) {
+            const SeqInfo s = dec_seq(a, n);
+            own = (int64_t)dec_blocks<M>(s, a.H) * dec_tiles(s);
+        }
+        int64_t sum = own;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const int64_t x = __shfl_up(sum, m, 64);
+            if (lane >= m) sum += x;
+        }
+        if (lane == 63) scan[w] = sum;
+        __syncthreads();
+        int64_t lo = before + sum - own, chunk = 0;
+        for (int i = 0; i < NW; ++i) {
+            if (i < w) lo += scan[i];
+            chunk += scan[i];
+        }
+        if (begin >= lo && begin < lo + own) {
+            found[0] = n;
+            found[1] = lo;
+        }
+        before += chunk;
+        __syncthreads();
+        if (before > begin) break;
+    }
+    int n = __builtin_amdgcn_readfirstlane((int)found[0]);
+    int64_t unit0 = found[1];   // tile number at which sequence n begins
+    int64_t pos = begin;
+
+    const uint32_t kc0 = lds_offset(kc), kr0 = lds_offset(kr);
+    // where this lane reads in a tile: key 16 kg + r, pieces 4 k + q (the exclusive or leaves bits 4
+    // and up of the piece alone, so four bases and fixed steps serve all k), the rope pieces, and for
+    // the transposed reads key 4 q + r / 4, the 8 bytes 4 (r & 3) .. of each column tile
+    int k_at[4], r_at[2], v_at[CT];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) k_at[k] = (16 * kg + r) * (LC * 2) + ((4 * k + q) ^ r) * 16;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) r_at[k] = (16 * kg + r) * (LR * 2) + ((4 * k + q) ^ ((r >> 1) & 7)) * 16;
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+        v_at[c] = (4 * q + (r >> 2)) * (LC * 2) + ((2 * (CT * w + c) + ((r >> 1) & 1)) ^ (4 * q + (r >> 2))) * 16 +
+                  (r & 1) * 8;
+    while (pos < end) {
+        const SeqInfo s = dec_seq(a, n);
+        const int tiles = dec_tiles(s), blocks = dec_blocks<M>(s, a.H);
+        if (pos >= unit0 + (int64_t)blocks * tiles) {
+            unit0 += (int64_t)blocks * tiles;
+            ++n;
+            continue;
+        }
+        const int rb = (int)((pos - unit0) / tiles);
+        const int t0 = (int)((pos - unit0) - (int64_t)rb * tiles);
+        const int t1 = (int)min((int64_t)tiles, t0 + (end - pos));
+        const int64_t rows = (int64_t)s.tokens * a.H;
+
+        // ---- q of this block's rows, and each row's key limit
+        bf16x8 qf[MQ][18];
+        int lim[MQ];
+#pragma unroll
+        for (int mt = 0; mt < MQ; ++mt) {
+            int64_t row = (int64_t)rb * M + 16 * (rh * MQ + mt) + r;
+            if (row >= rows) row = 0;
+            const int tok = (int)(row / a.H), h = (int)(row - (int64_t)tok * a.H);
+            lim[mt] = min(s.len, s.len - s.tokens + tok + 1);
+            const uint16_t* c = a.qc + (s.bos + tok) * a.qct + h * a.qch;
+            const uint16_t* p = a.qr + (s.bos + tok) * a.qrt + h * a.qrh;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) qf[mt][k] = *reinterpret_cast<const bf16x8*>(c + 32 * k + 8 * q);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) qf[mt][16 + k] = *reinterpret_cast<const bf16x8*>(p + 32 * k + 8 * q);
+        }
+        f32x4 o[MT][CT];
+        float m[MT], l[MQ];
+#pragma unroll
+        for (int mt = 0; mt < MQ; ++mt) l[mt] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            m[mt] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < CT; ++c) o[mt][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+
+        auto load_tile = [&](int buf, int row) {
+            // row: this lane's cache row of key 64 j + lane
+            const int lane16 = fresh(lane * 16);
+#pragma unroll
+            for (int i = 0; i < KPW; ++i) {
+                const int key = KPW * w + i;
+                const int from = __builtin_amdgcn_readlane(row, key);
+                if (from >= 0) {
+                    dma16(a.cache + (size_t)from * LROW, lane16 ^ ((key & 15) * 16),
+                          kc0 + buf * (DEC_KEYS * LC * 2) + key * (LC * 2));
+                } else {
+                    *reinterpret_cast<uint4*>(&kc[buf][key * (LC * 2) + lane16]) = make_uint4(0, 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < KPW / 8; ++i) {
+                const int key = KPW * w + 8 * i + (lane >> 3);
+                const int at = max(__shfl(row, key, 64), 0);   // scores of absent keys are replaced below
+                dma16(a.cache + (size_t)at * LROW + LC + (((lane & 7) ^ ((key >> 1) & 7)) * 8),
+                      kr0 + buf * (DEC_KEYS * LR * 2) + (KPW * w + 8 * i) * (LR * 2));
+            }
+        };
+
+        int row = dec_row(a, n, s.len, 64 * t0 + lane);
+        __syncthreads();   // the previous block's reads of LDS have ended
+        load_tile(0, row);
+        for (int j = t0; j < t1; ++j) {
+            const int buf = (j - t0) & 1;
+            const uint64_t there = __ballot(row >= 0);
+            const int next = j + 1 < t1 ? dec_row(a, n, s.len, 64 * (j + 1) + lane) : -1;
+            dma_wait();
+            __syncthreads();
+            if (j + 1 < t1) load_tile(buf ^ 1, next);
+            row = next;
+
+            // ---- S^T of this wave's 16 keys and row part
+            f32x4 sc[MQ];
+#pragma unroll
+            for (int mt = 0; mt < MQ; ++mt) sc[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            const char* kw = kc[buf];
+            const char* rw = kr[buf];
+#pragma unroll
+            for (int k = 0; k < 18; ++k) {
+                const bf16x8 f = k < 16 ? lds16(kw + k_at[k & 3] + (k >> 2) * 256) : lds16(rw + r_at[k - 16]);
+#pragma unroll
+                for (int mt = 0; mt < MQ; ++mt) sc[mt] = mfma32(f, qf[mt][k], sc[mt]);
+            }
+            const bool whole = there == ~0ull && 64 * j + 63 <= s.len - s.tokens;
+#pragma unroll
+            for (int mt = 0; mt < MQ; ++mt) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float v = sc[mt][i] * a.scale2;
+                    if (!whole) {
+                        const int key = 16 * kg + 4 * q + i;
+                        if (64 * j + key >= lim[mt] || !((there >> key) & 1)) v = -INFINITY;
+                    }
+                    sc[mt][i] = v;
+                }
+                float t = fmaxf(fmaxf(sc[mt][0], sc[mt][1]), fmaxf(sc[mt][2], sc[mt][3]));
+                t = fmaxf(t, __shfl_xor(t, 16, 64));
+                t = fmaxf(t, __shfl_xor(t, 32, 64));
+                if (q == 0) mx[kg][16 * (rh * MQ + mt) + r] = t;
+            }
+            lds_barrier();
+            // ---- the new maximum of every row, and this wave's weights
+            bool same = true;
+            float alpha[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int i = 16 * mt + r;
+                const float t = fmaxf(fmaxf(mx[0][i], mx[1][i]), fmaxf(mx[2][i], mx[3][i]));
+                const float now = fmaxf(m[mt], t);
+                alpha[mt] = ex2(m[mt] - (now == -INFINITY ? 0.f : now));
+                same = same && alpha[mt] == 1.f;
+                m[mt] = now;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MQ; ++mt) {
+                const float now = rh == 0 ? m[mt] : m[MT - MQ + mt];
+                const float ref = now == -INFINITY ? 0.f : now;
+                float p[4], sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = ex2(sc[mt][e] - ref);
+                    sum += p[e];
+                }
+                l[mt] = l[mt] * (rh == 0 ? alpha[mt] : alpha[MT - MQ + mt]) + sum;
+                *reinterpret_cast<uint2*>(&pf[((rh * MQ + mt) * 2 + (kg >> 1)) * 1024 + lane * 16 + (kg & 1) * 8]) =
+                    make_uint2(pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]));
+            }
+            if (!__all(same)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[mt][c][e] *= alpha[mt];
+            }
+            lds_barrier();
+            // ---- O^T of this wave's columns
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                bf16x8 p[MT];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) p[mt] = lds16(&pf[(mt * 2 + t) * 1024 + lane * 16]);
+                const char* v = kc[buf] + t * 32 * (LC * 2);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    const bf16x8 f = join8(lds_tr(v + v_at[c]), lds_tr(v + 16 * (LC * 2) + v_at[c]));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) o[mt][c] = mfma32(f, p[mt], o[mt][c]);
+                }
+            }
+        }
+        // ---- the row sums of all waves, then the output
+        __syncthreads();
+#pragma unroll
+        for (int mt = 0; mt < MQ; ++mt) {
+            float t = l[mt];
+            t += __shfl_xor(t, 16, 64);
+            t += __shfl_xor(t, 32, 64);
+            if (q == 0) mx[kg][16 * (rh * MQ + mt) + r] = t;
+        }
+        __syncthreads();
+        const bool direct = t0 == 0 && t1 == tiles;
+        const int slot = 2 * wg + (t0 == 0 ? 1 : 0);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int i = 16 * mt + r;
+            const float sum = (mx[0][i] + mx[1][i]) + (mx[2][i] + mx[3][i]);
+            const int64_t grow = (int64_t)rb * M + i;
+            if (grow >= rows) continue;
+            if (direct) {
+                const float inv = sum > 0.f ? 1.f / sum : sum;   // a row without keys gives zeros, NaN stays NaN
+                const size_t out = (size_t)s.bos * a.H + grow;
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+                    *reinterpret_cast<uint2*>(a.o + out * LC + 16 * (CT * w + c) + 4 * q) =
+                        make_uint2(pack_bf2(o[mt][c][0] * inv, o[mt][c][1] * inv),
+                                   pack_bf2(o[mt][c][2] * inv, o[mt][c][3] * inv));
+                if (a.lse && w == 0 && q == 0) a.lse[out] = sum == 0.f ? -INFINITY : LN2 * (m[mt] + lg2(sum));
+            } else {
+                float* part = a.part + ((size_t)slot * M + i) * LC + 16 * CT * w + 4 * q;
+#pragma unroll
+                for (int c = 0; c < CT; ++c) *reinterpret_cast<f32x4*>(part + 16 * c) = o[mt][c];
+                if (w == 0 && q == 0) a.part_ml[(size_t)slot * M + i] = make_float2(m[mt], sum);
+            }
+        }
+        if (t0 == 0 && t1 < tiles && tid == 0)
+            a.rec[wg] = make_int4(n, rb, (int)((pos + tiles - 1) / share), 0);
+        pos += t1 - t0;
+    }
+}
+
+// Joins the partial sums of a unit that was cut: workgroup (wg, row) takes one row of the unit that
+// began in workgroup wg's run, its four waves every fourth part each.
+template <int MT>
+__global__ __launch_bounds__(256) void latent_join_kernel(LatentDecodeArgs a) {
+    constexpr int M = 16 * MT;
+    __shared__ float sums[4][LC];
+    __shared__ float ml[4][2];
+    const int wg = blockIdx.x / M, i = blockIdx.x % M;
+    const int4 rec = a.rec[wg];
+    if (rec.x < 0) return;
+    const SeqInfo s = dec_seq(a, rec.x);
+    const int64_t grow = (int64_t)rec.y * M + i;
+    if (grow >= (int64_t)s.tokens * a.H) return;
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int parts = rec.z - wg + 1;
+    float m = -INFINITY, l = 0.f;
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int k = w; k < parts; k += 4) {
+        const size_t slot = k == 0 ? 2 * wg + 1 : 2 * (size_t)(wg + k);
+        const float2 pm = a.part_ml[slot * M + i];
+        const float4* p = reinterpret_cast<const float4*>(a.part + (slot * M + i) * LC) + 2 * lane;
+        const float4 x = p[0], y = p[1];
+        const float now = fmaxf(m, pm.x);
+        const float ref = now == -INFINITY ? 0.f : now;
+        const float fa = ex2(m - ref), fb = ex2(pm.x - ref);
+        m = now;
+        l = l * fa + pm.y * fb;
+        acc[0] = acc[0] * fa + x.x * fb;
+        acc[1] = acc[1] * fa + x.y * fb;
+        acc[2] = acc[2] * fa + x.z * fb;
+        acc[3] = acc[3] * fa + x.w * fb;
+        acc[4] = acc[4] * fa + y.x * fb;
+        acc[5] = acc[5] * fa + y.y * fb;
+        acc[6] = acc[6] * fa + y.z * fb;
+        acc[7] = acc[7] * fa + y.w * fb;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[w][8 * lane + e] = acc[e];
+    if (lane == 0) ml[w][0] = m, ml[w][1] = l;
+    __syncthreads();
+    float top = -INFINITY, sum = 0.f, f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k][0]);
+    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[k] = ex2(ml[k][0] - ref);
+        sum += ml[k][1] * f[k];
+    }
+    const float inv = sum > 0.f ? 1.f / sum : sum;
+    const size_t out = (size_t)s.bos * a.H + grow;
+    const int c = 2 * threadIdx.x;
+    float v[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        v[e] = ((sums[0][c + e] * f[0] + sums[1][c + e] * f[1]) + (sums[2][c + e] * f[2] + sums[3][c + e] * f[3])) * inv;
+    *reinterpret_cast<uint32_t*>(a.o + out * LC + c) = pack_bf2(v[0], v[1]);
+    if (a.lse && threadIdx.x == 0) a.lse[out] = sum == 0.f ? -INFINITY : LN2 * (top + lg2(sum));
+}
+
+// One wave a token: 64 16-byte pieces of the latent and 8 of the rope part into the cache row that
+// its slot names.
+__global__ __launch_bounds__(256) void latent_write_kernel(const uint16_t* c, const uint16_t* r, int64_t cs, int64_t rs,
+                                                           uint16_t* cache, const int32_t* slots, int T,
+                                                           int64_t num_slots) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= T) return;
+    const int slot = slots[t];
+    if (slot < 0 || slot >= num_slots) return;
+    uint16_t* to = cache + (size_t)slot * LROW;
+    const uint4 v = *reinterpret_cast<const uint4*>(c + t * cs + 8 * lane);
+    *reinterpret_cast<uint4*>(to + 8 * lane) = v;
+    if (lane < LR / 8)
+        *reinterpret_cast<uint4*>(to + LC + 8 * lane) = *reinterpret_cast<const uint4*>(r + t * rs + 8 * lane);
+}
+
+// Rows of a block: the fewest of 16, 32 and 64 that hold the rows of a sequence (of an average one
+// in a packed batch); more rows would be computed for nothing, fewer would read the keys again.
+int dec_m(const cdr_latent_decode_problem* p) {
+    const int64_t tokens = p->varlen ? ((int64_t)p->T + p->N - 1) / p->N : p->T;
+    const int64_t rows = tokens * p->H;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+template <int MT, int NW>
+hipError_t launch_latent_decode(const LatentDecodeArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((latent_decode_kernel<MT, NW>), dim3(DEC_GRID), dim3(64 * NW), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((latent_join_kernel<MT>), dim3(DEC_GRID * 16 * MT), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+bool mult8(int64_t x) { return (x & 7) == 0; }
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+}  // namespace
+
+}  // namespace cdr
+
+extern "C" {
+
+cdr_status cdr_latent_decode_check(const cdr_latent_decode_problem* p) {
+    if (p == nullptr) return CDR_ERR_NULL_ARG;
+    if (p->N <= 0 || p->T < 0 || p->H <= 0 || p->num_pages <= 0 || p->page_size <= 0 || p->table_cols <= 0)
+        return CDR_ERR_BAD_SHAPE;
+    if (p->page_size & (p->page_size - 1)) return CDR_ERR_UNSUPPORTED;
+    if ((int64_t)p->num_pages * p->page_size > INT32_MAX) return CDR_ERR_BAD_SHAPE;
+    if ((p->varlen ? 1 : (int64_t)p->N) * p->T * p->H > INT32_MAX) return CDR_ERR_BAD_SHAPE;
+    for (int i = 0; i < 2; ++i)
+        if (!cdr::mult8(p->qc_stride[i]) || !cdr::mult8(p->qr_stride[i])) return CDR_ERR_UNSUPPORTED;
+    return CDR_OK;
+}
+
+size_t cdr_latent_decode_workspace_bytes(const cdr_latent_decode_problem* p) {
+    if (cdr_latent_decode_check(p) != CDR_OK) return 0;
+    const size_t rows = 2 * (size_t)cdr::DEC_GRID * cdr::dec_m(p);
+    return rows * (cdr::LC * sizeof(float) + sizeof(float2)) + cdr::DEC_GRID * sizeof(int4);
+}
+
+cdr_status cdr_latent_decode_fwd(const cdr_latent_decode_problem* p, const void* q_latent, const void* q_rope,
+                                 const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                                 const int32_t* cu_seqlens, void* o, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+    const cdr_status st = cdr_latent_decode_check(p);
+    if (st != CDR_OK) return st;
+    if (p->T == 0) return CDR_OK;
+    if (!q_latent || !q_rope || !cache || !block_table || !seq_lens || !o || (p->varlen && !cu_seqlens))
+        return CDR_ERR_NULL_ARG;
+    if (!cdr::aligned16(q_latent) || !cdr::aligned16(q_rope) || !cdr::aligned16(cache) || !cdr::aligned16(o))
+        return CDR_ERR_UNSUPPORTED;
+    if (!workspace || !cdr::aligned16(workspace) || workspace_bytes < cdr_latent_decode_workspace_bytes(p))
+        return CDR_ERR_WORKSPACE;
+    cdr::LatentDecodeArgs a;
+    a.qc = static_cast<const uint16_t*>(q_latent);
+    a.qr = static_cast<const uint16_t*>(q_rope);
+    a.cache = static_cast<const uint16_t*>(cache);
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.cu = p->varlen ? cu_seqlens : nullptr;
+    a.o = static_cast<uint16_t*>(o);
+    a.lse = lse;
+    const int m = cdr::dec_m(p);
+    const size_t rows = 2 * (size_t)cdr::DEC_GRID * m;
+    a.part = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part + rows * cdr::LC);
+    a.rec = reinterpret_cast<int4*>(a.part_ml + rows);
+    a.qct = p->qc_stride[0], a.qch = p->qc_stride[1];
+    a.qrt = p->qr_stride[0], a.qrh = p->qr_stride[1];
+    a.N = p->N, a.T = p->T, a.H = p->H;
+    a.cols = p->table_cols;
+    a.num_pages = p->num_pages;
+    a.shift = __builtin_ctz((unsigned)p->page_size);
+    a.scale2 = p->scale * cdr::LOG2E;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = m == 16   ? cdr::launch_latent_decode<1, 4>(a, s)
+                         : m == 32 ? cdr::launch_latent_decode<2, 4>(a, s)
+                                   : cdr::launch_latent_decode<4, 8>(a, s);
+    return e == hipSuccess ? CDR_OK : CDR_ERR_HIP;
+}
+
+cdr_status cdr_latent_cache_write(int32_t T, int32_t num_pages, int32_t page_size, const void* c, const void* k_rope,
+                                  int64_t c_stride, int64_t k_rope_stride, void* cache, const int32_t* slot_map,
+                                  void* stream) {
+    if (T < 0 || num_pages <= 0 || page_size <= 0) return CDR_ERR_BAD_SHAPE;
+    if (!cdr::mult8(c_stride) || !cdr::mult8(k_rope_stride)) return CDR_ERR_UNSUPPORTED;
+    if (T == 0) return CDR_OK;
+    if (!c || !k_rope || !cache || !slot_map) return CDR_ERR_NULL_ARG;
+    if (!cdr::aligned16(c) || !cdr::aligned16(k_rope) || !cdr::aligned16(cache)) return CDR_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL(cdr::latent_write_kernel, dim3((unsigned)(((int64_t)T + 3) / 4)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), static_cast<const uint16_t*>(c),
+                       static_cast<const uint16_t*>(k_rope), c_stride, k_rope_stride, static_cast<uint16_t*>(cache),
+                       slot_map, T, (int64_t)num_pages * page_size);
+    return hipGetLastError() == hipSuccess ? CDR_OK : CDR_ERR_HIP;
+}
+
+}  // extern "C"

@@ -35,8 +35,9 @@
  *  - Errors are returned as cdr_status values; nothing is printed or thrown.
  *
  * Beside the operator stand the parts of a block and of a serving step that touch it: the norms,
- * gate and residual at a block's boundary (cdr_block_norm_*), and the offsets, page tables and
- * slots of a step from its request lengths (cdr_build_page_tables).
+ * gate and residual at a block's boundary (cdr_block_norm_*), the offsets, page tables and slots
+ * of a step from its request lengths (cdr_build_page_tables), and latent attention, the softmax
+ * attention of hybrid stacks: over a paged cache in the absorbed form (cdr_latent_decode_*).
  */
 #ifndef CHUNK_DR_H
 #define CHUNK_DR_H
@@ -521,6 +522,76 @@ cdr_status cdr_build_page_tables(int32_t N, int32_t table_cols, int32_t num_free
                                  const int32_t* free_pages, const int32_t* free_head, int32_t* free_head_out,
                                  int32_t* cu_seqlens, int32_t* seq_lens, int32_t* positions, int32_t* slot_map,
                                  int32_t* shortage, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Latent attention, absorbed form, over a paged cache (decode and a few draft tokens).
+ *
+ * A cached key is CDR_LATENT_DIM + CDR_LATENT_ROPE = 512 + 64 bf16, one for all heads: the latent
+ * c_j, which is the value too, and the rope part r_j.  q_latent is the query with the key's
+ * up-projection absorbed.  For token i of sequence n's L_n new tokens and every head,
+ *
+ *     o = sum_j p_j c_j,   p = softmax over j < seq_lens[n] - L_n + i + 1 of
+ *                              scale (q_latent . c_j + q_rope . r_j)
+ *     lse = log of the sum of exp of those scores (natural)
+ *
+ * so seq_lens counts the new tokens, whose keys are written first (cdr_latent_cache_write).  Key j
+ * of sequence n is row block_table[n, j / page_size] * page_size + j % page_size of the cache.
+ * Keys beyond table_cols * page_size and keys whose page lies outside [0, num_pages) do not exist:
+ * they are masked and not read.  A row left without keys gives o = 0 and lse = -inf.  What lies
+ * behind a sequence's last key, in its last page or elsewhere, does not affect it, whatever it
+ * holds; keys below seq_lens[n] must be finite, those that a row's causal limit hides from it
+ * too (they meet a weight of zero).
+ *
+ *   q_latent   bf16 [tokens, H, 512], q_rope bf16 [tokens, H, 64]: strides (token, head) in
+ *              elements, multiples of 8; tokens = N * T, or T in all when varlen
+ *   cache      bf16 [num_pages, page_size, 576], page_size a power of two
+ *   block_table int32 [N, table_cols], seq_lens int32 [N], cu_seqlens int32 [N + 1] (varlen;
+ *              offsets are clipped to [0, T])
+ *   o          bf16 [tokens, H, 512], lse fp32 [tokens, H] or NULL; rows behind the last sequence
+ *              are left as they were
+ *   workspace  at least cdr_latent_decode_workspace_bytes(p) bytes, 16-byte aligned, contents
+ *              irrelevant, not to be used by another call until this one's kernels have finished
+ * q, cache, o and the workspace are 16-byte aligned.  Scores and sums are fp32; the weights p_j
+ * enter the second product as bf16 (the first product's sum of them does not).  Lengths are read on
+ * the device, so a captured call serves any lengths.  Repeated calls give the same bits.
+ * ------------------------------------------------------------------------------------------ */
+#define CDR_LATENT_DIM 512
+#define CDR_LATENT_ROPE 64
+
+typedef struct {
+    int32_t N;                  /* sequences */
+    int32_t T;                  /* new tokens of each sequence (all packed tokens when varlen) */
+    int32_t H;                  /* heads */
+    int32_t varlen;             /* cu_seqlens is read when non-zero */
+    int32_t num_pages;
+    int32_t page_size;          /* a power of two; num_pages * page_size < 2^31 */
+    int32_t table_cols;         /* columns of block_table */
+    float scale;
+    int64_t qc_stride[2];       /* q_latent: token, head */
+    int64_t qr_stride[2];       /* q_rope: token, head */
+} cdr_latent_decode_problem;
+
+/* Host-only validation of a latent decode problem. */
+cdr_status cdr_latent_decode_check(const cdr_latent_decode_problem* p);
+
+size_t cdr_latent_decode_workspace_bytes(const cdr_latent_decode_problem* p);
+
+/* Two kernels on `stream`. */
+cdr_status cdr_latent_decode_fwd(const cdr_latent_decode_problem* p, const void* q_latent, const void* q_rope,
+                                 const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                                 const int32_t* cu_seqlens, void* o, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * Writes T tokens' latents into the cache: row slot_map[t] of cache [num_pages * page_size, 576]
+ * becomes (c[t], k_rope[t]).  Slots outside the cache are skipped (padding, as
+ * cdr_build_page_tables marks it with -1); two tokens with one slot give an undefined row.
+ *   c bf16 [T, 512], k_rope bf16 [T, 64]: token strides in elements, multiples of 8; c, k_rope
+ *   and cache 16-byte aligned; slot_map int32 [T]
+ */
+cdr_status cdr_latent_cache_write(int32_t T, int32_t num_pages, int32_t page_size, const void* c, const void* k_rope,
+                                  int64_t c_stride, int64_t k_rope_stride, void* cache, const int32_t* slot_map,
+                                  void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* cdr_status_str(cdr_status s);

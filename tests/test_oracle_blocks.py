@@ -158,3 +158,82 @@ def test_pages_binding_errors():
                     (ValueError, dict(free_pages=i32(3, 3))), (ValueError, dict())):
         with pytest.raises(bad):
             cdr.build_page_tables(**{**good, **kw})
+
+
+# ------------------------------------------------------------------------------ latent attention
+
+def test_latent_decode_oracle_matches_a_plain_softmax():
+    """One sequence on pages in order is plain attention over [c, r] with values c."""
+    from oracle import latent
+    g = torch.Generator().manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    qc, qr, cache = r(1, 2, 3, 512), r(1, 2, 3, 64), r(3, 4, 576)
+    table = torch.arange(3, dtype=torch.int32)[None]
+    o, lse, mag, _ = latent.decode(qc, qr, cache, table, torch.tensor([9], dtype=torch.int32), 0.1)
+    keys = cache.reshape(12, 576)[:9]
+    s = torch.einsum("thd,jd->thj", torch.cat([qc, qr], -1)[0], keys) * 0.1
+    s[0, :, 8] = float("-inf")
+    p = torch.softmax(s, -1)
+    assert torch.allclose(o[0], p @ keys[:, :512]) and torch.allclose(lse[0], torch.logsumexp(s, -1))
+    assert (o.abs() <= mag + 1e-12).all()
+
+
+def test_latent_decode_struct_and_check():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(ops.__file__), "..", "include", "chunk_dr.h")).read()
+    body = re.search(r"typedef struct \{([^{}]*)\} cdr_latent_decode_problem;", text).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    fields = re.findall(r"(?:int32_t|int64_t|float)\s+(\w+)(?:\[2\])?;", body)
+    assert fields == [f[0] for f in ops.cdr_latent_decode_problem._fields_]
+    lib = cdr.load_library()
+    ok = dict(N=2, T=1, H=16, varlen=0, num_pages=8, page_size=16, table_cols=4, scale=1.0)
+    for kw, status in ((dict(), 0), (dict(N=0), 2), (dict(T=-1), 2), (dict(H=0), 2), (dict(num_pages=0), 2),
+                       (dict(page_size=0), 2), (dict(table_cols=0), 2), (dict(page_size=12), 3),
+                       (dict(num_pages=2 ** 30), 2), (dict(T=2 ** 28), 2), (dict(T=0), 0)):
+        p = ops.cdr_latent_decode_problem(*{**ok, **kw}.values())
+        assert lib.cdr_latent_decode_check(ctypes.byref(p)) == status, kw
+        assert (lib.cdr_latent_decode_workspace_bytes(ctypes.byref(p)) > 0) == (status == 0)
+    p = ops.cdr_latent_decode_problem(*ok.values())
+    fake = 1 << 20
+    args = [fake] * 5 + [None, fake, None, fake]
+    big = 1 << 40
+    for i in (0, 1, 2, 3, 4, 6):
+        bad = list(args)
+        bad[i] = None
+        assert lib.cdr_latent_decode_fwd(ctypes.byref(p), *bad, big, None) == 1, i
+    assert lib.cdr_latent_decode_fwd(ctypes.byref(p), *args, 64, None) == 5
+    bad = list(args)
+    bad[2] = fake + 8
+    assert lib.cdr_latent_decode_fwd(ctypes.byref(p), *bad, big, None) == 3
+    p.qc_stride[1] = 4
+    assert lib.cdr_latent_decode_fwd(ctypes.byref(p), *args, big, None) == 3
+    p = ops.cdr_latent_decode_problem(*{**ok, "varlen": 1}.values())
+    assert lib.cdr_latent_decode_fwd(ctypes.byref(p), *args, big, None) == 1     # no cu_seqlens
+    assert lib.cdr_latent_cache_write(1, 0, 16, fake, fake, 512, 64, fake, fake, None) == 2
+    assert lib.cdr_latent_cache_write(-1, 1, 16, fake, fake, 512, 64, fake, fake, None) == 2
+    assert lib.cdr_latent_cache_write(1, 1, 16, fake, fake, 12, 64, fake, fake, None) == 3
+    assert lib.cdr_latent_cache_write(1, 1, 16, None, fake, 512, 64, fake, fake, None) == 1
+    assert lib.cdr_latent_cache_write(1, 1, 16, fake, fake + 2, 512, 64, fake, fake, None) == 3
+
+
+def test_latent_decode_binding_errors():
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    good = dict(q_latent=b(2, 1, 4, 512), q_rope=b(2, 1, 4, 64), cache=b(3, 16, 576), block_table=i(2, 2),
+                seq_lens=i(2), scale=0.1)
+    for bad, kw in ((ValueError, dict(q_latent=b(2, 1, 4, 256))), (TypeError, dict(q_latent=b(2, 1, 4, 512).float())),
+                    (ValueError, dict(q_rope=b(2, 1, 3, 64))), (ValueError, dict(cache=b(3, 16, 512))),
+                    (ValueError, dict(cache=b(3, 12, 576))), (TypeError, dict(block_table=i(2, 2).long())),
+                    (ValueError, dict(block_table=i(3, 2))), (ValueError, dict(seq_lens=i(3))),
+                    (ValueError, dict(cu_seqlens=i(3))), (ValueError, dict(out=b(2, 1, 512, 4).transpose(2, 3))),
+                    (TypeError, dict(lse_out=b(2, 1, 4))), (ValueError, dict())):
+        with pytest.raises(bad):
+            cdr.latent_decode_fwd(**{**good, **kw})
+    for bad, args in ((ValueError, (b(3, 512), b(3, 64), b(3, 16, 576), i(2))),
+                      (ValueError, (b(3, 256), b(3, 64), b(3, 16, 576), i(3))),
+                      (ValueError, (b(3, 512), b(2, 64), b(3, 16, 576), i(3))),
+                      (TypeError, (b(3, 512), b(3, 64), b(3, 16, 576), i(3).long())),
+                      (ValueError, (b(3, 512), b(3, 64), b(3, 16, 576), i(3)))):
+        with pytest.raises(bad):
+            cdr.latent_cache_write(*args)
