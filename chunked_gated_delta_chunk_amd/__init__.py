@@ -9,4 +9,5 @@ from .ops import (chunk_dr_fwd, PreparedForward, load_library, workspace_bytes, 
                   BWD_PREP, BWD_CHAINS, BWD_LOCAL, BWD_ALL, segment_map, merge_states,
                   chunk_dr_fwd_noalloc, NOALLOC_SCRATCH_BYTES, check_cu_seqlens)
 from .blocks import block_norm_fwd, block_norm_bwd, build_page_tables, PageTables  # noqa: F401
-from .latent import latent_cache_write, latent_decode_fwd, latent_decode_workspace_bytes  # noqa: F401
+from .latent import (latent_cache_write, latent_decode_fwd, latent_decode_workspace_bytes,  # noqa: F401
+                     latent_attn_fwd, latent_attn_bwd)

@@ -13,7 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libchunkdr.so")
 SOURCES = ["cdr_api.hip", "cdr_intra.hip", "cdr_chain.hip", "cdr_decode.hip", "cdr_bwd.hip", "cdr_cp.hip",
            "cdr_noalloc.hip", "cdr_norm.hip", "cdr_pages.hip",
-           "cdr_latent.hip"]
+           "cdr_latent.hip", "cdr_latent_attn.hip"]
 ARCH = os.environ.get("CDR_OFFLOAD_ARCH", "gfx950")
 
 

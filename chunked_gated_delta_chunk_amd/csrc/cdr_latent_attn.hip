@@ -1,0 +1,639 @@
+// Latent attention in the expanded form: prefill and training.
+//
+//     s_ij = scale (qn_i . kn_j + qr_i . kr_j)     qn, kn: 128 dimensions a head, qr, kr: 64, kr one
+//     o_i  = sum_j p_ij v_j,  p = softmax(s)        for all heads; v: 128; causal, the last row of a
+//     lse_i = log sum_j exp s_ij                    sequence sees all its keys
+//
+// and with delta_i = do_i . o_i, ds_ij = p_ij (do_i . v_j - delta_i):
+//
+//     dv_j = sum_i p_ij do_i,   dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i,
+//     dkr_j = the rope part of dk_j summed over the heads.
+//
+// All products run on 32x32x16 MFMA with fp32 accumulators; p and ds enter the next product as bf16
+// (8 bits of each weight, the same as the outputs carry).  What bounds them is the matrix rate, so the
+// layout is chosen to feed it:
+//  - A wave owns 32 rows (keys in the dk/dv kernel) whose operands stay in registers; the tiles of
+//    the other side stream through LDS two deep, by copies that need no registers.
+//  - Products are taken transposed where that puts the owned index in the lane (S^T = K Q^T): the
+//    softmax statistics are then a lane's own, and the result's registers are, in the order
+//    8 (i / 4) + 4 (lane / 32) + i % 4, directly the right operand of the next product.  No weights
+//    pass through LDS.  The other operand of that product comes through the transposing read.
+//  - 16-byte pieces of a tile row are stored at piece ^ f(row), with f one to one on 16 rows: both the
+//    row reads and the transposing reads then use all banks.
+//
+// The backward computes the scores twice, once for dq (rows in the lanes) and once for dk and dv
+// (keys in the lanes), rather than adding dq's parts by atomics, whose order would change the
+// result; dkr's parts are written a head each and added in order.
+#include "chunk_dr.h"
+#include "cdr_latent.h"
+
+namespace cdr {
+
+namespace {
+
+constexpr int AN = 128;       // nope dimensions
+constexpr int AV = 128;       // value dimensions
+constexpr int AQ = AN + LR;   // a query's
+constexpr int A_ROWS = 128;   // rows (or keys) of a workgroup
+constexpr int A_TILE = 64;    // rows of a streamed tile
+
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
+
+__device__ __forceinline__ f32x16 mma(const bf16x8& a, const bf16x8& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = 0.f;
+    return z;
+}
+// registers 8 t .. 8 t + 7 of a result as the right operand of the next product
+__device__ __forceinline__ bf16x8 operand(const f32x16& p, int t) {
+    const uint4 v = make_uint4(pack_bf2(p[8 * t], p[8 * t + 1]), pack_bf2(p[8 * t + 2], p[8 * t + 3]),
+                               pack_bf2(p[8 * t + 4], p[8 * t + 5]), pack_bf2(p[8 * t + 6], p[8 * t + 7]));
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+struct LatentAttnArgs {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* kr;
+    const uint16_t* v;
+    const int32_t* cuq;
+    const int32_t* cuk;
+    const uint16_t* d_o;
+    const float* delta;
+    uint16_t* o;        // forward: o; dq kernel: dq
+    float* lse;
+    uint16_t* dk;
+    uint16_t* dv;
+    float* dkr;         // [H][Tk total][64]
+    int64_t qt, qh, kt, kh, rt, vt, vh;   // strides, elements
+    int T, Tk, H, N, slots, total_k;
+    float scale, scale2;
+};
+
+// offsets within a tile: row pitch 256 bytes (16 pieces) and 128 bytes (8 pieces)
+__device__ __forceinline__ int f16(int row) { return ((row & 7) << 1) | ((row >> 3) & 1); }
+__device__ __forceinline__ int f8(int row) { return (((row >> 1) & 3) << 1) | ((row >> 3) & 1); }
+
+struct Seq {
+    int64_t q0, k0;    // first row and key
+    int lq, lk;
+};
+
+__device__ __forceinline__ Seq attn_seq(const LatentAttnArgs& a, int n) {
+    Seq s;
+    if (a.cuq) {
+        const int qb = min(max(a.cuq[n], 0), a.T), kb = min(max(a.cuk[n], 0), a.Tk);
+        s.q0 = qb, s.k0 = kb;
+        s.lq = min(max(a.cuq[n + 1], qb), a.T) - qb;
+        s.lk = min(max(a.cuk[n + 1], kb), a.Tk) - kb;
+    } else {
+        s.q0 = (int64_t)n * a.T, s.k0 = (int64_t)n * a.Tk;
+        s.lq = a.T, s.lk = a.Tk;
+    }
+    return s;
+}
+
+// Sequence and block of a slot: as in the chunk map, sequence n owns the slots from
+// cu[n] / A_ROWS + n on (packed), or n * ceil(T / A_ROWS) on.  False for an unused slot.
+__device__ __forceinline__ bool attn_slot(const LatentAttnArgs& a, const int32_t* cu, int T, int slot, int& n, int& block) {
+    if (cu == nullptr) {
+        const int per = (T + A_ROWS - 1) / A_ROWS;
+        n = slot / per;
+        block = slot - n * per;
+        return true;
+    }
+    int lo = 0, hi = a.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (min(max(cu[mid], 0), T) / A_ROWS + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    n = lo;
+    const int b = min(max(cu[n], 0), T);
+    block = slot - (b / A_ROWS + n);
+    return block >= 0 && block * A_ROWS < min(max(cu[n + 1], b), T) - b;
+}
+
+// Copies rows `first` .. + 63 (clipped to `last`) of an array with 256-byte or 128-byte rows to LDS:
+// this wave's quarter.  base: row 0; stride: bytes between rows.
+__device__ __forceinline__ void copy256(const void* base, int64_t first, int64_t last, uint32_t stride, uint32_t lds, int w,
+                                        int lane) {
+    const char* b = static_cast<const char*>(base) + first * stride;
+    const int top = (int)min(last - first, (int64_t)63);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 4 * (w + 4 * i) + (lane >> 4);
+        const uint32_t off = __umul24(min(row, top), stride) + (((lane & 15) ^ f16(row)) * 16);
+        dma16(b, off, lds + 1024 * (w + 4 * i));
+    }
+}
+__device__ __forceinline__ void copy128(const void* base, int64_t first, int64_t last, uint32_t stride, uint32_t lds, int w,
+                                        int lane) {
+    const char* b = static_cast<const char*>(base) + first * stride;
+    const int top = (int)min(last - first, (int64_t)63);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = 8 * (w + 4 * i) + (lane >> 3);
+        const uint32_t off = __umul24(min(row, top), stride) + (((lane & 7) ^ f8(row)) * 16);
+        dma16(b, off, lds + 1024 * (w + 4 * i));
+    }
+}
+
+// left operand of 16 contracted dimensions (step s): rows 32 t + (lane & 31) of a tile
+__device__ __forceinline__ bf16x8 row256(const char* tile, int t, int s, int lane) {
+    const int r = lane & 31;
+    return lds16(tile + t * 32 * 256 + r * 256 + (((2 * s + (lane >> 5)) ^ f16(r)) * 16));
+}
+__device__ __forceinline__ bf16x8 row128(const char* tile, int t, int s, int lane) {
+    const int r = lane & 31;
+    return lds16(tile + t * 32 * 128 + r * 128 + (((2 * s + (lane >> 5)) ^ f8(r)) * 16));
+}
+// left operand of 16 contracted rows (step s: rows 16 s ..) for columns 32 c + (lane & 31) of a tile, the
+// rows in the order 8 (i / 4) + 4 (lane / 32) + i % 4 of a result's registers
+__device__ __forceinline__ bf16x8 col256(const char* tile, int s, int c, int lane) {
+    const int i = lane & 15, row = 4 * (lane >> 5) + (i >> 2);
+    const int piece = 4 * c + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
+    const char* p = tile + (16 * s + row) * 256 + (i & 1) * 8;
+    return join8(lds_tr(p + ((piece ^ f16(row)) * 16)), lds_tr(p + 8 * 256 + ((piece ^ f16(row + 8)) * 16)));
+}
+__device__ __forceinline__ bf16x8 col128(const char* tile, int s, int c, int lane) {
+    const int i = lane & 15, row = 4 * (lane >> 5) + (i >> 2);
+    const int piece = 4 * c + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
+    const char* p = tile + (16 * s + row) * 128 + (i & 1) * 8;
+    return join8(lds_tr(p + ((piece ^ f8(row)) * 16)), lds_tr(p + 8 * 128 + ((piece ^ f8(row + 8)) * 16)));
+}
+
+// four neighbouring columns of a transposed result as bf16
+__device__ __forceinline__ void put4(uint16_t* p, const f32x16& x, int g, float f) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf2(x[4 * g] * f, x[4 * g + 1] * f), pack_bf2(x[4 * g + 2] * f, x[4 * g + 3] * f));
+}
+
+// What the forward and the dq kernel share: a workgroup's 128 rows, streamed keys and values.
+struct Tiles {
+    uint32_t kn, kr, v;   // LDS offsets of buffer 0
+};
+
+__device__ __forceinline__ void load_keys(const LatentAttnArgs& a, const Seq& s, int h, int tile, int buf, const Tiles& at,
+                                          int w, int lane) {
+    const int64_t first = (int64_t)tile * A_TILE, last = s.lk - 1;
+    copy256(a.k + s.k0 * a.kt + h * a.kh, first, last, (uint32_t)a.kt * 2, at.kn + buf * A_TILE * 256, w, lane);
+    copy128(a.kr + s.k0 * a.rt, first, last, (uint32_t)a.rt * 2, at.kr + buf * A_TILE * 128, w, lane);
+    copy256(a.v + s.k0 * a.vt + h * a.vh, first, last, (uint32_t)a.vt * 2, at.v + buf * A_TILE * 256, w, lane);
+}
+
+__global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
+    __shared__ __align__(256) char lds[2 * A_TILE * (256 + 128 + 256)];
+    char* kn = lds;
+    char* kr = kn + 2 * A_TILE * 256;
+    char* vt = kr + 2 * A_TILE * 128;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = blockIdx.x % a.H;
+    int n, block;
+    if (!attn_slot(a, a.cuq, a.T, a.slots - 1 - blockIdx.x / a.H, n, block)) return;
+    const Seq s = attn_seq(a, n);
+    const Tiles at = {lds_offset(kn), lds_offset(kr), lds_offset(vt)};
+
+    // this lane's row, and the keys it sees
+    const int row = block * A_ROWS + 32 * w + (lane & 31);
+    const int use = min(row, s.lq - 1);
+    const int lim = min(s.lk, s.lk - s.lq + use + 1);
+    const int lim_first = min(s.lk, s.lk - s.lq + min(block * A_ROWS + 32 * w, s.lq - 1) + 1);
+    const int lim_last = min(s.lk, s.lk - s.lq + min(block * A_ROWS + 32 * w + 31, s.lq - 1) + 1);
+    const int keys = min(s.lk, s.lk - s.lq + min(block * A_ROWS + A_ROWS - 1, s.lq - 1) + 1);
+    const int tiles = keys > 0 ? (keys + A_TILE - 1) / A_TILE : 0;
+
+    bf16x8 qf[12];
+    {
+        const uint16_t* q = a.q + (s.q0 + use) * a.qt + h * a.qh + 8 * (lane >> 5);
+#pragma unroll
+        for (int k = 0; k < 12; ++k) qf[k] = *reinterpret_cast<const bf16x8*>(q + 16 * k);
+    }
+    f32x16 o[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] = zero16();
+    float m = -INFINITY, l = 0.f;
+
+    if (tiles > 0) load_keys(a, s, h, 0, 0, at, w, lane);
+    for (int j = 0; j < tiles; ++j) {
+        const int buf = j & 1;
+        dma_wait();
+        __syncthreads();
+        if (j + 1 < tiles) load_keys(a, s, h, j + 1, buf ^ 1, at, w, lane);
+        if (j * A_TILE >= lim_last) continue;   // all of this wave's rows end before this tile
+        const char* tn = kn + buf * A_TILE * 256;
+        const char* tr = kr + buf * A_TILE * 128;
+        const char* tv = vt + buf * A_TILE * 256;
+        f32x16 sc[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            sc[t] = zero16();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sc[t] = mma(row256(tn, t, k, lane), qf[k], sc[t]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[t] = mma(row128(tr, t, k, lane), qf[8 + k], sc[t]);
+        }
+        if ((j + 1) * A_TILE > lim_first) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (j * A_TILE + 32 * t + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= lim) sc[t][i] = -INFINITY;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[t][i]);
+        top = fmaxf(top, __shfl_xor(top, 32, 64)) * a.scale2;
+        const float now = fmaxf(m, top);
+        const float ref = now == -INFINITY ? 0.f : now;
+        const float alpha = ex2(m - ref);
+        m = now;
+        float sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                sc[t][i] = ex2(sc[t][i] * a.scale2 - ref);
+                sum += sc[t][i];
+            }
+        l = l * alpha + sum;
+        if (!__all(alpha == 1.f)) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[c][i] *= alpha;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bf16x8 p = operand(sc[t], u);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[c] = mma(col256(tv, 2 * t + u, c, lane), p, o[c]);
+            }
+    }
+    l += __shfl_xor(l, 32, 64);
+    if (row >= s.lq) return;
+    const float inv = l > 0.f ? 1.f / l : l;   // a row without keys gives zeros, NaN stays NaN
+    const size_t out = (size_t)(s.q0 + row) * a.H + h;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) put4(a.o + out * AV + 32 * c + 8 * g + 4 * (lane >> 5), o[c], g, inv);
+    if (lane < 32) a.lse[out] = l == 0.f ? -INFINITY : LN2 * (m + lg2(l));
+}
+
+// delta = do . o of every row and head: 16 lanes a row
+__global__ __launch_bounds__(256) void latent_delta_kernel(const uint16_t* o, const uint16_t* d_o, float* delta, int64_t rows) {
+    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int i = threadIdx.x & 15;
+    float x[8], y[8], t = 0.f;
+    if (row < rows) {
+        unpack8(*reinterpret_cast<const uint4*>(o + row * AV + 8 * i), x);
+        unpack8(*reinterpret_cast<const uint4*>(d_o + row * AV + 8 * i), y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t += x[e] * y[e];
+    }
+#pragma unroll
+    for (int k = 1; k < 16; k <<= 1) t += __shfl_xor(t, k, 64);
+    if (row < rows && i == 0) delta[row] = t;
+}
+
+__global__ __launch_bounds__(256, 2) void latent_dq_kernel(LatentAttnArgs a) {
+    __shared__ __align__(256) char lds[2 * A_TILE * (256 + 128 + 256)];
+    char* kn = lds;
+    char* kr = kn + 2 * A_TILE * 256;
+    char* vt = kr + 2 * A_TILE * 128;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = blockIdx.x % a.H;
+    int n, block;
+    if (!attn_slot(a, a.cuq, a.T, a.slots - 1 - blockIdx.x / a.H, n, block)) return;
+    const Seq s = attn_seq(a, n);
+    const Tiles at = {lds_offset(kn), lds_offset(kr), lds_offset(vt)};
+    const int row = block * A_ROWS + 32 * w + (lane & 31);
+    const int use = min(row, s.lq - 1);
+    const int lim = min(s.lk, s.lk - s.lq + use + 1);
+    const int lim_first = min(s.lk, s.lk - s.lq + min(block * A_ROWS + 32 * w, s.lq - 1) + 1);
+    const int lim_last = min(s.lk, s.lk - s.lq + min(block * A_ROWS + 32 * w + 31, s.lq - 1) + 1);
+    const int keys = min(s.lk, s.lk - s.lq + min(block * A_ROWS + A_ROWS - 1, s.lq - 1) + 1);
+    const int tiles = keys > 0 ? (keys + A_TILE - 1) / A_TILE : 0;
+
+    const size_t in = (size_t)(s.q0 + use) * a.H + h;
+    bf16x8 qf[12], df[8];
+    {
+        const uint16_t* q = a.q + (s.q0 + use) * a.qt + h * a.qh + 8 * (lane >> 5);
+#pragma unroll
+        for (int k = 0; k < 12; ++k) qf[k] = *reinterpret_cast<const bf16x8*>(q + 16 * k);
+        const uint16_t* d = a.d_o + in * AV + 8 * (lane >> 5);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) df[k] = *reinterpret_cast<const bf16x8*>(d + 16 * k);
+    }
+    float lse = a.lse[in] * LOG2E;
+    if (lse == -INFINITY) lse = INFINITY;   // a row without keys: all its weights are zero
+    const float delta = a.delta[in];
+    f32x16 dq[6];
+#pragma unroll
+    for (int c = 0; c < 6; ++c) dq[c] = zero16();
+
+    if (tiles > 0) load_keys(a, s, h, 0, 0, at, w, lane);
+    for (int j = 0; j < tiles; ++j) {
+        const int buf = j & 1;
+        dma_wait();
+        __syncthreads();
+        if (j + 1 < tiles) load_keys(a, s, h, j + 1, buf ^ 1, at, w, lane);
+        const char* tn = kn + buf * A_TILE * 256;
+        const char* tr = kr + buf * A_TILE * 128;
+        const char* tv = vt + buf * A_TILE * 256;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (j * A_TILE + 32 * t >= lim_last) break;
+            f32x16 sc = zero16(), dp = zero16();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sc = mma(row256(tn, t, k, lane), qf[k], sc);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc = mma(row128(tr, t, k, lane), qf[8 + k], sc);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dp = mma(row256(tv, t, k, lane), df[k], dp);
+            const bool cut = j * A_TILE + 32 * t + 32 > lim_first;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float p = ex2(sc[i] * a.scale2 - lse);
+                if (cut && j * A_TILE + 32 * t + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= lim) p = 0.f;
+                dp[i] = p * (dp[i] - delta);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bf16x8 d = operand(dp, u);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) dq[c] = mma(col256(tn, 2 * t + u, c, lane), d, dq[c]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) dq[4 + c] = mma(col128(tr, 2 * t + u, c, lane), d, dq[4 + c]);
+            }
+        }
+    }
+    if (row >= s.lq) return;
+    const size_t out = (size_t)(s.q0 + row) * a.H + h;
+#pragma unroll
+    for (int c = 0; c < 6; ++c)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) put4(a.o + out * AQ + 32 * c + 8 * g + 4 * (lane >> 5), dq[c], g, a.scale);
+}
+
+__global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
+    __shared__ __align__(256) char lds[2 * A_TILE * (256 + 128 + 256)];
+    __shared__ __align__(16) float stat[2][2][A_TILE];   // lse (base 2) and delta of a tile's rows
+    char* qn = lds;
+    char* qr = qn + 2 * A_TILE * 256;
+    char* td = qr + 2 * A_TILE * 128;
+    const uint32_t qn0 = lds_offset(qn), qr0 = lds_offset(qr), td0 = lds_offset(td);
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = blockIdx.x % a.H;
+    int n, block;
+    if (!attn_slot(a, a.cuk, a.Tk, blockIdx.x / a.H, n, block)) return;
+    const Seq s = attn_seq(a, n);
+    const int key = block * A_ROWS + 32 * w + (lane & 31);
+    const int use = min(key, s.lk - 1);
+    const int shift = s.lk - s.lq;                          // row i sees keys up to i + shift
+    const int first_row = max(0, block * A_ROWS - shift);   // the first row that sees a key of this block
+    const int j0 = first_row / A_TILE, tiles = (s.lq + A_TILE - 1) / A_TILE;
+
+    bf16x8 kf[12], vf[8];
+    {
+        const uint16_t* k = a.k + (s.k0 + use) * a.kt + h * a.kh + 8 * (lane >> 5);
+        const uint16_t* r = a.kr + (s.k0 + use) * a.rt + 8 * (lane >> 5);
+        const uint16_t* v = a.v + (s.k0 + use) * a.vt + h * a.vh + 8 * (lane >> 5);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) kf[i] = *reinterpret_cast<const bf16x8*>(k + 16 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kf[8 + i] = *reinterpret_cast<const bf16x8*>(r + 16 * i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) vf[i] = *reinterpret_cast<const bf16x8*>(v + 16 * i);
+    }
+    f32x16 dk[6], dv[4];
+#pragma unroll
+    for (int c = 0; c < 6; ++c) dk[c] = zero16();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) dv[c] = zero16();
+
+    auto load_rows = [&](int tile, int buf) {
+        const int64_t first = (int64_t)tile * A_TILE, last = s.lq - 1;
+        const uint16_t* q = a.q + s.q0 * a.qt + h * a.qh;
+        copy256(q, first, last, (uint32_t)a.qt * 2, qn0 + buf * A_TILE * 256, w, lane);
+        copy128(q + AN, first, last, (uint32_t)a.qt * 2, qr0 + buf * A_TILE * 128, w, lane);
+        copy256(a.d_o + ((size_t)s.q0 * a.H + h) * AV, first, last, (uint32_t)a.H * AV * 2, td0 + buf * A_TILE * 256, w, lane);
+        if (w < 2) {
+            // wave 0: lse, so that a row behind the end or without keys has weights of zero; wave 1: delta
+            const int64_t r = first + lane;
+            const size_t at = (size_t)(s.q0 + min(r, last)) * a.H + h;
+            float x = w == 0 ? a.lse[at] * LOG2E : a.delta[at];
+            if (w == 0 && (r > last || x == -INFINITY)) x = INFINITY;
+            stat[buf][w][lane] = x;
+        }
+    };
+
+    if (j0 < tiles) load_rows(j0, 0);
+    for (int j = j0; j < tiles; ++j) {
+        const int buf = (j - j0) & 1;
+        dma_wait();
+        __syncthreads();
+        if (j + 1 < tiles) load_rows(j + 1, buf ^ 1);
+        const char* tn = qn + buf * A_TILE * 256;
+        const char* tr = qr + buf * A_TILE * 128;
+        const char* to = td + buf * A_TILE * 256;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int r0 = j * A_TILE + 32 * t;
+            if (r0 + 31 + shift < block * A_ROWS + 32 * w) continue;   // no row here sees these keys
+            f32x16 sc = zero16(), dp = zero16();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sc = mma(row256(tn, t, k, lane), kf[k], sc);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc = mma(row128(tr, t, k, lane), kf[8 + k], sc);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dp = mma(row256(to, t, k, lane), vf[k], dp);
+            // a key behind the sequence's end is computed like its last and not stored
+            const bool cut = r0 + shift < block * A_ROWS + 32 * w + 31;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 ls = *reinterpret_cast<const f32x4*>(&stat[buf][0][32 * t + 8 * g + 4 * (lane >> 5)]);
+                const f32x4 de = *reinterpret_cast<const f32x4*>(&stat[buf][1][32 * t + 8 * g + 4 * (lane >> 5)]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 4 * g + e;
+                    float p = ex2(sc[i] * a.scale2 - ls[e]);
+                    if (cut && r0 + 8 * g + 4 * (lane >> 5) + e + shift < key) p = 0.f;
+                    sc[i] = p;
+                    dp[i] = p * (dp[i] - de[e]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bf16x8 p = operand(sc, u), d = operand(dp, u);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) dv[c] = mma(col256(to, 2 * t + u, c, lane), p, dv[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) dk[c] = mma(col256(tn, 2 * t + u, c, lane), d, dk[c]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) dk[4 + c] = mma(col128(tr, 2 * t + u, c, lane), d, dk[4 + c]);
+            }
+        }
+    }
+    if (key >= s.lk) return;
+    const size_t out = (size_t)(s.k0 + key) * a.H + h;
+    const int c4 = 4 * (lane >> 5);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            put4(a.dv + out * AV + 32 * c + 8 * g + c4, dv[c], g, 1.f);
+            put4(a.dk + out * AN + 32 * c + 8 * g + c4, dk[c], g, a.scale);
+        }
+    float* r = a.dkr + ((size_t)h * a.total_k + s.k0 + key) * LR;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x16& x = dk[4 + c];
+            *reinterpret_cast<float4*>(r + 32 * c + 8 * g + c4) =
+                make_float4(x[4 * g] * a.scale, x[4 * g + 1] * a.scale, x[4 * g + 2] * a.scale, x[4 * g + 3] * a.scale);
+        }
+}
+
+// dkr: the heads' parts added in order, 4 dimensions a thread
+__global__ __launch_bounds__(256) void latent_dkr_kernel(const float* part, uint16_t* dkr, const int32_t* cuk, int N, int total,
+                                                         int H) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t keys = cuk ? min(max(cuk[N], 0), total) : total;
+    if (i >= keys * (LR / 4)) return;
+    f32x4 t = {0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < H; ++h) t += *reinterpret_cast<const f32x4*>(part + ((size_t)h * total) * LR + 4 * i);
+    *reinterpret_cast<uint2*>(dkr + 4 * i) = make_uint2(pack_bf2(t[0], t[1]), pack_bf2(t[2], t[3]));
+}
+
+int64_t total_q(const cdr_latent_attn_problem* p) { return p->varlen ? p->T : (int64_t)p->N * p->T; }
+int64_t total_k(const cdr_latent_attn_problem* p) { return p->varlen ? p->Tk : (int64_t)p->N * p->Tk; }
+
+int64_t attn_slots(int64_t T, const cdr_latent_attn_problem* p) {
+    return p->varlen ? T / A_ROWS + p->N : p->N * ((T + A_ROWS - 1) / A_ROWS);
+}
+
+bool ok_stride(int64_t s) { return s >= 0 && (s & 7) == 0 && s < (1 << 23); }
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+LatentAttnArgs attn_args(const cdr_latent_attn_problem* p, const void* q, const void* k, const void* kr, const void* v,
+                         const int32_t* cuq, const int32_t* cuk) {
+    LatentAttnArgs a = {};
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint16_t*>(k);
+    a.kr = static_cast<const uint16_t*>(kr);
+    a.v = static_cast<const uint16_t*>(v);
+    a.cuq = p->varlen ? cuq : nullptr;
+    a.cuk = p->varlen ? cuk : nullptr;
+    a.qt = p->q_stride[0], a.qh = p->q_stride[1];
+    a.kt = p->k_stride[0], a.kh = p->k_stride[1];
+    a.rt = p->k_rope_stride;
+    a.vt = p->v_stride[0], a.vh = p->v_stride[1];
+    a.T = p->T, a.Tk = p->Tk, a.H = p->H, a.N = p->N;
+    a.total_k = (int)total_k(p);
+    a.scale = p->scale;
+    a.scale2 = p->scale * LOG2E;
+    return a;
+}
+
+size_t up16(size_t x) { return (x + 15) / 16 * 16; }
+
+}  // namespace
+
+}  // namespace cdr
+
+extern "C" {
+
+cdr_status cdr_latent_attn_check(const cdr_latent_attn_problem* p) {
+    if (p == nullptr) return CDR_ERR_NULL_ARG;
+    if (p->N <= 0 || p->T < 0 || p->Tk < 0 || p->H <= 0) return CDR_ERR_BAD_SHAPE;
+    if (!(p->scale > 0.f) || p->scale > 3.0e38f) return CDR_ERR_BAD_SHAPE;
+    if (p->H > (1 << 15)) return CDR_ERR_UNSUPPORTED;
+    const int64_t tq = cdr::total_q(p), tk = cdr::total_k(p);
+    if (tq * p->H > INT32_MAX || tk * p->H > INT32_MAX) return CDR_ERR_BAD_SHAPE;
+    if (cdr::attn_slots(p->T, p) * p->H > INT32_MAX || cdr::attn_slots(p->Tk, p) * p->H > INT32_MAX) return CDR_ERR_BAD_SHAPE;
+    for (int i = 0; i < 2; ++i)
+        if (!cdr::ok_stride(p->q_stride[i]) || !cdr::ok_stride(p->k_stride[i]) || !cdr::ok_stride(p->v_stride[i]))
+            return CDR_ERR_UNSUPPORTED;
+    if (!cdr::ok_stride(p->k_rope_stride)) return CDR_ERR_UNSUPPORTED;
+    return CDR_OK;
+}
+
+cdr_status cdr_latent_attn_fwd(const cdr_latent_attn_problem* p, const void* q, const void* k_nope, const void* k_rope,
+                               const void* v, const int32_t* cu_seqlens, const int32_t* cu_seqlens_k, void* o, float* lse,
+                               void* stream) {
+    const cdr_status st = cdr_latent_attn_check(p);
+    if (st != CDR_OK) return st;
+    if (cdr::total_q(p) == 0) return CDR_OK;
+    if (!q || !o || !lse || (p->varlen && (!cu_seqlens || !cu_seqlens_k))) return CDR_ERR_NULL_ARG;
+    if (cdr::total_k(p) > 0 && (!k_nope || !k_rope || !v)) return CDR_ERR_NULL_ARG;
+    if (!cdr::aligned16(q) || !cdr::aligned16(k_nope) || !cdr::aligned16(k_rope) || !cdr::aligned16(v) || !cdr::aligned16(o))
+        return CDR_ERR_UNSUPPORTED;
+    cdr::LatentAttnArgs a = cdr::attn_args(p, q, k_nope, k_rope, v, cu_seqlens, cu_seqlens_k);
+    a.o = static_cast<uint16_t*>(o);
+    a.lse = lse;
+    a.slots = (int)cdr::attn_slots(p->T, p);
+    hipLaunchKernelGGL(cdr::latent_fwd_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), a);
+    return hipGetLastError() == hipSuccess ? CDR_OK : CDR_ERR_HIP;
+}
+
+size_t cdr_latent_attn_bwd_workspace_bytes(const cdr_latent_attn_problem* p) {
+    if (cdr_latent_attn_check(p) != CDR_OK) return 0;
+    return cdr::up16((size_t)cdr::total_q(p) * p->H * sizeof(float)) + (size_t)cdr::total_k(p) * p->H * cdr::LR * sizeof(float);
+}
+
+cdr_status cdr_latent_attn_bwd(const cdr_latent_attn_problem* p, const void* q, const void* k_nope, const void* k_rope,
+                               const void* v, const int32_t* cu_seqlens, const int32_t* cu_seqlens_k, const void* o,
+                               const float* lse, const void* d_o, void* dq, void* dk_nope, void* dk_rope, void* dv,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    const cdr_status st = cdr_latent_attn_check(p);
+    if (st != CDR_OK) return st;
+    const int64_t tq = cdr::total_q(p), tk = cdr::total_k(p);
+    if (p->varlen && (!cu_seqlens || !cu_seqlens_k)) return CDR_ERR_NULL_ARG;
+    if (tq > 0 && (!q || !o || !lse || !d_o || !dq)) return CDR_ERR_NULL_ARG;
+    if (tk > 0 && (!k_nope || !k_rope || !v || !dk_nope || !dk_rope || !dv)) return CDR_ERR_NULL_ARG;
+    const void* all[] = {q, k_nope, k_rope, v, o, d_o, dq, dk_nope, dk_rope, dv};
+    for (const void* x : all)
+        if (!cdr::aligned16(x)) return CDR_ERR_UNSUPPORTED;
+    const size_t need = cdr_latent_attn_bwd_workspace_bytes(p);
+    if (need > 0 && (!workspace || !cdr::aligned16(workspace) || workspace_bytes < need)) return CDR_ERR_WORKSPACE;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    cdr::LatentAttnArgs a = cdr::attn_args(p, q, k_nope, k_rope, v, cu_seqlens, cu_seqlens_k);
+    float* delta = static_cast<float*>(workspace);
+    a.delta = delta;
+    a.dkr = reinterpret_cast<float*>(static_cast<char*>(workspace) + cdr::up16((size_t)tq * p->H * sizeof(float)));
+    a.lse = const_cast<float*>(lse);
+    a.d_o = static_cast<const uint16_t*>(d_o);
+    a.o = static_cast<uint16_t*>(dq);
+    a.dk = static_cast<uint16_t*>(dk_nope);
+    a.dv = static_cast<uint16_t*>(dv);
+    if (tq > 0) {
+        const int64_t rows = tq * p->H;
+        hipLaunchKernelGGL(cdr::latent_delta_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, s,
+                           static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(d_o), delta, rows);
+        if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
+        a.slots = (int)cdr::attn_slots(p->T, p);
+        hipLaunchKernelGGL(cdr::latent_dq_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a);
+        if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
+    }
+    if (tk > 0) {
+        a.slots = (int)cdr::attn_slots(p->Tk, p);
+        hipLaunchKernelGGL(cdr::latent_dkv_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a);
+        if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
+        hipLaunchKernelGGL(cdr::latent_dkr_kernel, dim3((unsigned)((tk * (cdr::LR / 4) + 255) / 256)), dim3(256), 0, s, a.dkr,
+                           static_cast<uint16_t*>(dk_rope), a.cuk, p->N, (int)tk, p->H);
+        if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
+    }
+    return CDR_OK;
+}
+
+}  // extern "C"

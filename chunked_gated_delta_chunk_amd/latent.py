@@ -1,5 +1,5 @@
 """Python binding of latent attention (cdr_latent_* of include/chunk_dr.h): the absorbed form over a
-paged cache, for decoding.
+paged cache, for decoding, and the expanded form with its gradients, for prefill and training.
 
 Argument marshalling only, as in ops.py.
 """
@@ -164,3 +164,135 @@ def latent_decode_fwd(q_latent: torch.Tensor, q_rope: torch.Tensor, cache: torch
     if st != CDR_OK:
         _raise(st, "latent_decode_fwd")
     return out, lse_out
+
+
+NOPE_DIM, VALUE_DIM = 128, 128
+QUERY_DIM = NOPE_DIM + LATENT_ROPE
+
+
+class _LatentAttn:
+    """The checked inputs of the expanded form: its problem struct and the tensors it points to."""
+
+    def __init__(self, q, k_nope, k_rope, v, scale, cu_seqlens, cu_seqlens_k, what):
+        self.lib = load_library()
+        if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[3] != QUERY_DIM:
+            raise ValueError("q must be [B, T, H, 192]")
+        B, T, H = q.shape[:3]
+        if not isinstance(k_nope, torch.Tensor) or k_nope.dim() != 4:
+            raise ValueError("k_nope must be [B, Tk, H, 128]")
+        Tk = k_nope.shape[1]
+        q = _part(q, "q", (B, T, H, QUERY_DIM))
+        k_nope = _part(k_nope, "k_nope", (B, Tk, H, NOPE_DIM))
+        k_rope = _part(k_rope, "k_rope", (B, Tk, LATENT_ROPE))
+        v = _part(v, "v", (B, Tk, H, VALUE_DIM))
+        N = B
+        if cu_seqlens is None and cu_seqlens_k is not None:
+            raise ValueError("cu_seqlens_k needs cu_seqlens")
+        if cu_seqlens is not None:
+            if cu_seqlens_k is None:
+                if Tk != T:
+                    raise ValueError("cu_seqlens_k is required where keys and queries differ in number")
+                cu_seqlens_k = cu_seqlens
+            for name, t in (("cu_seqlens", cu_seqlens), ("cu_seqlens_k", cu_seqlens_k)):
+                _need(t, name, torch.int32)
+                if t.dim() != 1 or t.numel() < 2:
+                    raise ValueError(f"{name} must be a 1-D tensor of N + 1 offsets")
+            N = cu_seqlens.numel() - 1
+            if cu_seqlens_k.numel() != N + 1:
+                raise ValueError("cu_seqlens and cu_seqlens_k differ in length")
+            if B != 1:
+                raise ValueError("cu_seqlens requires B == 1")
+            cu_seqlens, cu_seqlens_k = cu_seqlens.contiguous(), cu_seqlens_k.contiguous()
+        self.device = q.device
+        _on(self.device, k_nope=k_nope, k_rope=k_rope, v=v, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k)
+        q, qt = _tokens(q)
+        k_nope, kt = _tokens(k_nope)
+        k_rope, rt = _tokens(k_rope)
+        v, vt = _tokens(v)
+        self.B, self.T, self.Tk, self.H = B, T, Tk, H
+        p = ops.cdr_latent_attn_problem(N, T, Tk, H, int(cu_seqlens is not None),
+                                        QUERY_DIM ** -0.5 if scale is None else float(scale))
+        p.q_stride[0], p.q_stride[1] = qt, q.stride(2)
+        p.k_stride[0], p.k_stride[1] = kt, k_nope.stride(2)
+        p.v_stride[0], p.v_stride[1] = vt, v.stride(2)
+        p.k_rope_stride = rt
+        st = self.lib.cdr_latent_attn_check(ctypes.byref(p))
+        if st != CDR_OK:
+            _raise(st, what)
+        self.p = p
+        self.tensors = (q, k_nope, k_rope, v, cu_seqlens, cu_seqlens_k)
+        self.inputs = tuple(_ptr(t) for t in self.tensors)
+
+
+def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor,
+                    scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                    cu_seqlens_k: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    lse_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal latent attention in the expanded form (prefill and training).
+
+    ``q [B,T,H,192]`` (nope, then rope part), ``k_nope [B,Tk,H,128]``, ``k_rope [B,Tk,64]`` (one for
+    all heads), ``v [B,Tk,H,128]`` bf16; k_nope and v may be slices of one projection.  The last
+    query sees all Tk keys, so ``Tk - T`` earlier keys are a context; a query without keys gives
+    zeros and -inf.  Packed batches have B = 1, ``cu_seqlens`` int32 ``[N+1]`` for the queries and
+    ``cu_seqlens_k`` for the keys (the same when None).  ``scale=None`` means ``192 ** -0.5``; it must
+    be positive.  Returns ``(o, lse)``: ``[B,T,H,128]`` bf16 and ``[B,T,H]`` fp32.  ``out`` and
+    ``lse_out`` optionally supply the buffers; rows behind the last packed sequence are left as they
+    were in them.
+    """
+    c = _LatentAttn(q, k_nope, k_rope, v, scale, cu_seqlens, cu_seqlens_k, "latent_attn_fwd")
+    if out is not None:
+        _need(out, "out", torch.bfloat16, (c.B, c.T, c.H, VALUE_DIM), dense=True)
+        if out.data_ptr() % 16:
+            raise ValueError("out must be 16-byte aligned")
+    if lse_out is not None:
+        _need(lse_out, "lse_out", torch.float32, (c.B, c.T, c.H), dense=True)
+    _on(c.device, out=out, lse_out=lse_out)
+    stream, current = _gpu(c.device)
+    if out is None:
+        out = torch.empty((c.B, c.T, c.H, VALUE_DIM), dtype=torch.bfloat16, device=c.device)
+    if lse_out is None:
+        lse_out = torch.empty((c.B, c.T, c.H), dtype=torch.float32, device=c.device)
+    with current:
+        st = c.lib.cdr_latent_attn_fwd(ctypes.byref(c.p), *c.inputs, _ptr(out), _ptr(lse_out), stream)
+    if st != CDR_OK:
+        _raise(st, "latent_attn_fwd")
+    return out, lse_out
+
+
+def latent_attn_bwd(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                    lse: torch.Tensor, do: torch.Tensor, scale: Optional[float] = None,
+                    cu_seqlens: Optional[torch.Tensor] = None, cu_seqlens_k: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None):
+    """Gradients of :func:`latent_attn_fwd`.
+
+    Inputs as the forward, its ``o`` and ``lse``, and ``do [B,T,H,128]`` bf16, the gradient of o.
+    Returns bf16 ``(dq, dk_nope, dk_rope, dv)`` with the shapes of the inputs; dk_rope is the sum
+    over the heads, added in fp32.  Repeated calls give the same bits.  ``workspace`` optionally
+    supplies the scratch buffer (uint8, contiguous).
+    """
+    c = _LatentAttn(q, k_nope, k_rope, v, scale, cu_seqlens, cu_seqlens_k, "latent_attn_bwd")
+    shape = (c.B, c.T, c.H, VALUE_DIM)
+    _need(o, "o", torch.bfloat16, shape)
+    _need(do, "do", torch.bfloat16, shape)
+    _need(lse, "lse", torch.float32, shape[:3])
+    _on(c.device, o=o, do=do, lse=lse, workspace=workspace)
+    stream, current = _gpu(c.device)
+    o, lse, do = ops._aligned(o), lse.contiguous(), ops._aligned(do)
+    need = c.lib.cdr_latent_attn_bwd_workspace_bytes(ctypes.byref(c.p))
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=c.device)
+    elif workspace.numel() * workspace.element_size() < need:
+        raise ValueError("workspace too small")
+    elif not workspace.is_contiguous() or workspace.data_ptr() % 16:
+        raise ValueError("workspace must be contiguous and 16-byte aligned")
+    empty = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=c.device)  # noqa: E731
+    dq = empty(c.B, c.T, c.H, QUERY_DIM)
+    dk, dv = empty(c.B, c.Tk, c.H, NOPE_DIM), empty(c.B, c.Tk, c.H, VALUE_DIM)
+    dkr = empty(c.B, c.Tk, LATENT_ROPE)
+    with current:
+        st = c.lib.cdr_latent_attn_bwd(ctypes.byref(c.p), *c.inputs, _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk),
+                                       _ptr(dkr), _ptr(dv), _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), stream)
+    if st != CDR_OK:
+        _raise(st, "latent_attn_bwd")
+    return dq, dk, dkr, dv

@@ -28,7 +28,8 @@ EXPORTED = ("cdr_check", "cdr_workspace_bytes", "chunk_dr_fwd", "chunk_dr_fwd_st
             "cdr_block_norm_check", "cdr_block_norm_fwd", "cdr_block_norm_bwd_workspace_bytes",
             "cdr_block_norm_bwd", "cdr_page_tables_workspace_bytes", "cdr_build_page_tables",
             "cdr_latent_decode_check", "cdr_latent_decode_workspace_bytes", "cdr_latent_decode_fwd",
-            "cdr_latent_cache_write", "cdr_status_str", "cdr_version")
+            "cdr_latent_cache_write", "cdr_latent_attn_check", "cdr_latent_attn_fwd",
+            "cdr_latent_attn_bwd_workspace_bytes", "cdr_latent_attn_bwd", "cdr_status_str", "cdr_version")
 STATE_SEPARATE, STATE_POOL, STATE_POOL_SPEC = 0, 1, 2
 STAGE_INTRA, STAGE_CHAIN, STAGE_OUTPUT, STAGE_ALL = 1, 2, 4, 7
 NOALLOC_SCRATCH_BYTES = 256 * 1024 * 1024   # CDR_NOALLOC_SCRATCH_BYTES of chunk_dr.h
@@ -70,6 +71,13 @@ class cdr_latent_decode_problem(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("table_cols", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("qc_stride", ctypes.c_int64 * 2),
                 ("qr_stride", ctypes.c_int64 * 2)]
+
+
+class cdr_latent_attn_problem(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("T", ctypes.c_int32), ("Tk", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("varlen", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2),
+                ("v_stride", ctypes.c_int64 * 2), ("k_rope_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -136,6 +144,15 @@ def load_library(path: str = LIB_PATH):
     lib.cdr_latent_decode_fwd.restype = ctypes.c_int
     lib.cdr_latent_cache_write.argtypes = [ctypes.c_int32] * 3 + [vp, vp, ctypes.c_int64, ctypes.c_int64, vp, vp, vp]
     lib.cdr_latent_cache_write.restype = ctypes.c_int
+    AP = ctypes.POINTER(cdr_latent_attn_problem)
+    lib.cdr_latent_attn_check.argtypes = [AP]
+    lib.cdr_latent_attn_check.restype = ctypes.c_int
+    lib.cdr_latent_attn_fwd.argtypes = [AP] + [vp] * 9
+    lib.cdr_latent_attn_fwd.restype = ctypes.c_int
+    lib.cdr_latent_attn_bwd_workspace_bytes.argtypes = [AP]
+    lib.cdr_latent_attn_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.cdr_latent_attn_bwd.argtypes = [AP] + [vp] * 14 + [ctypes.c_size_t, vp]
+    lib.cdr_latent_attn_bwd.restype = ctypes.c_int
     lib.cdr_status_str.argtypes = [ctypes.c_int]
     lib.cdr_status_str.restype = ctypes.c_char_p
     lib.cdr_version.argtypes = []

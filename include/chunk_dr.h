@@ -37,7 +37,8 @@
  * Beside the operator stand the parts of a block and of a serving step that touch it: the norms,
  * gate and residual at a block's boundary (cdr_block_norm_*), the offsets, page tables and slots
  * of a step from its request lengths (cdr_build_page_tables), and latent attention, the softmax
- * attention of hybrid stacks: over a paged cache in the absorbed form (cdr_latent_decode_*).
+ * attention of hybrid stacks: over a paged cache in the absorbed form (cdr_latent_decode_*), and
+ * over packed sequences in the expanded form, with its gradients (cdr_latent_attn_*).
  */
 #ifndef CHUNK_DR_H
 #define CHUNK_DR_H
@@ -592,6 +593,75 @@ cdr_status cdr_latent_decode_fwd(const cdr_latent_decode_problem* p, const void*
 cdr_status cdr_latent_cache_write(int32_t T, int32_t num_pages, int32_t page_size, const void* c, const void* k_rope,
                                   int64_t c_stride, int64_t k_rope_stride, void* cache, const int32_t* slot_map,
                                   void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Latent attention, expanded form, over packed or equal-length sequences: prefill and training.
+ *
+ * Every head has its own keys and values, expanded from the latents, and all heads share the rope
+ * part of the key.  For row i of sequence n's L_q rows and its L_k keys (causal; the last row sees
+ * all keys, so L_k - L_q earlier keys are a context),
+ *
+ *     o_i = sum_j p_ij v_j,  p_i = softmax over j < L_k - L_q + i + 1 of
+ *                                  scale (q_i[:128] . k_nope_j + q_i[128:] . k_rope_j)
+ *     lse_i = log of the sum of exp of those scores (natural)
+ *
+ * A row without keys (L_q > L_k) gives o = 0 and lse = -inf, and no gradient.
+ *
+ *   q        bf16 [tokens, H, 192]: nope, then rope part     strides (token, head)
+ *   k_nope   bf16 [keys, H, 128]                             strides (token, head)
+ *   k_rope   bf16 [keys, 64]                                 stride of a token
+ *   v        bf16 [keys, H, 128]                             strides (token, head)
+ *   cu_seqlens, cu_seqlens_k  int32 [N + 1], varlen: rows' and keys' offsets, clipped to [0, T] and
+ *            [0, Tk]; may be the same array.  Else every sequence has T rows and Tk keys.
+ *   o        bf16 [tokens, H, 128], lse fp32 [tokens, H]; dense.  Rows behind the last sequence are
+ *            left as they were.
+ * Strides are in elements, multiples of 8, not negative and below 2^23, so k_nope and v may be the
+ * two halves of one projection [keys, H, 256]; all but lse are 16-byte aligned.  scale is positive.
+ * Values of a sequence must be finite, also those that the causal limit hides from a row (they meet
+ * weights of zero); those of other sequences do not matter.  Scores and sums are fp32, the weights
+ * enter the second product as bf16.  Repeated calls give the same bits.
+ * ------------------------------------------------------------------------------------------ */
+#define CDR_LATENT_NOPE 128
+#define CDR_LATENT_VALUE 128
+
+typedef struct {
+    int32_t N;                  /* sequences */
+    int32_t T;                  /* rows of each sequence (all packed rows when varlen) */
+    int32_t Tk;                 /* keys of each sequence (all packed keys when varlen) */
+    int32_t H;                  /* heads, at most 32768 */
+    int32_t varlen;             /* cu_seqlens and cu_seqlens_k are read when non-zero */
+    float scale;
+    int64_t q_stride[2];        /* token, head */
+    int64_t k_stride[2];
+    int64_t v_stride[2];
+    int64_t k_rope_stride;      /* token */
+} cdr_latent_attn_problem;
+
+/* Host-only validation of a latent attention problem. */
+cdr_status cdr_latent_attn_check(const cdr_latent_attn_problem* p);
+
+/* One kernel on `stream`, no workspace. */
+cdr_status cdr_latent_attn_fwd(const cdr_latent_attn_problem* p, const void* q, const void* k_nope, const void* k_rope,
+                               const void* v, const int32_t* cu_seqlens, const int32_t* cu_seqlens_k, void* o, float* lse,
+                               void* stream);
+
+/*
+ * Gradients of L = sum(o * d_o), from the forward's o and lse.
+ *
+ *   o, lse    as the forward wrote them;  d_o bf16 [tokens, H, 128] dense
+ *   dq        bf16 [tokens, H, 192], dk_nope bf16 [keys, H, 128], dk_rope bf16 [keys, 64] (the sum
+ *             over the heads, added in fp32), dv bf16 [keys, H, 128]; dense.  Rows and keys behind the
+ *             last sequence are left as they were.
+ *   workspace at least cdr_latent_attn_bwd_workspace_bytes(p) bytes, 16-byte aligned, contents
+ *             irrelevant, not to be used by another call until this one's kernels have finished
+ * No output may overlap an input.  No atomics: repeated calls give the same bits.
+ */
+size_t cdr_latent_attn_bwd_workspace_bytes(const cdr_latent_attn_problem* p);
+
+cdr_status cdr_latent_attn_bwd(const cdr_latent_attn_problem* p, const void* q, const void* k_nope, const void* k_rope,
+                               const void* v, const int32_t* cu_seqlens, const int32_t* cu_seqlens_k, const void* o,
+                               const float* lse, const void* d_o, void* dq, void* dk_nope, void* dk_rope, void* dv,
+                               void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* cdr_status_str(cdr_status s);

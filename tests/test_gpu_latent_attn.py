@@ -1,0 +1,244 @@
+"""Latent attention in the expanded form on the GPU against the fp64 oracle, forward and gradients.
+
+Tolerances.  A score is 192 exact products of bf16 added in fp32 and scaled: an error of at most
+e = (193 + 8) 2^-24 times the sum of its absolute terms (`size`).  Weights p have relative error
+2 e + 2^-18 (e in the score and in the statistics; exponential, sum of at most 4096 in a lane and 8
+levels of tree) before they are rounded to bf16 (2^-8).  With `mag` the sum of the absolute terms of an
+output's last product:
+
+  o, dv     (2^-8 + 2 e + 2^-16) mag + half a step of the value
+  dq, dk    dS = p (dP - delta): p as above; dP has 2^-16 of its absolute terms, delta is formed from o
+            as the forward rounded it, (2^-8 + 2^-8 + 2 e + 2^-16) of its absolute terms; dS is rounded
+            to bf16: 2^-8; together (4 2^-8 + 4 e + 2^-14) mag + half a step
+"""
+import math
+
+import pytest
+import torch
+
+import chunked_gated_delta_chunk_amd as cdr
+from oracle import latent as oracle_latent
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16 = torch.bfloat16
+NAMES = ("dq", "dk_nope", "dk_rope", "dv")
+
+
+def make(lq, lk, H, seed, packed=True, spare=0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g).to(BF16)  # noqa: E731
+    if packed:
+        B, T, Tk = 1, sum(lq) + spare, sum(lk) + spare
+        cu = lambda x: torch.tensor([0] + list(x)).cumsum(0).to(torch.int32)  # noqa: E731
+        more = dict(cu_seqlens=cu(lq), cu_seqlens_k=cu(lk))
+    else:
+        B, T, Tk, more = len(lq), lq[0], lk[0], {}
+    kv = r(B, Tk, H, 256)
+    return dict(q=r(B, T, H, 192), k_nope=kv[..., :128], k_rope=r(B, Tk, 64), v=kv[..., 128:], **more), r(B, T, H, 128)
+
+
+def dev(kw):
+    """On the GPU with the same strides."""
+    out = {}
+    for k, v in kw.items():
+        if isinstance(v, torch.Tensor) and k in ("k_nope", "v") and not v.is_contiguous():
+            base = torch.empty(v.shape[:3] + (256,), dtype=BF16, device=DEV)
+            view = base[..., :128] if k == "k_nope" else base[..., 128:]
+            view.copy_(v)
+            out[k] = view
+        else:
+            out[k] = v.to(DEV) if isinstance(v, torch.Tensor) else v
+    return out
+
+
+def within(name, got, ref, tol, live):
+    d = ((got.cpu().double() - ref).abs() / tol)[live]
+    assert not d.numel() or float(d.max()) <= 1, f"{name}: {float(d.max()):.3f} of the tolerance"
+
+
+def compare(kw, do, o, lse, grads, scale):
+    ref = oracle_latent.attention(scale=scale, do=do, **kw)
+    live = ~torch.isnan(ref["lse"])
+    empty = live & torch.isinf(ref["lse"])
+    full = live & ~empty
+    assert torch.isfinite(o.cpu()[live]).all()
+    assert (o.cpu()[empty] == 0).all() and (lse.cpu()[empty] == -math.inf).all()
+    e = 201 * 2.0 ** -24 * ref["size"]
+    within("lse", lse, ref["lse"], e + 2.0 ** -18 + 2.0 ** -22 * ref["lse"].abs(), full)
+    top = float(e[live].max()) if live.any() else 0.0     # keys meet many rows: the largest of them
+    tol = lambda n, f, x: (f * 2.0 ** -8 + x * top + 2.0 ** -14) * ref[n + "_mag"] \
+        + 2.0 ** -8 * ref[n].abs() + 1e-30  # noqa: E731
+    within("o", o, ref["o"], tol("o", 1, 2), live)
+    if grads is None:
+        return
+    for name, g in zip(NAMES, grads):
+        keys = ~torch.isnan(ref[name])
+        assert torch.isfinite(g.cpu()[keys]).all(), name
+        within(name, g, ref[name], tol(name, 1 if name == "dv" else 4, 2 if name == "dv" else 4), keys)
+
+
+def run(kw, do, scale=192 ** -0.5):
+    d = dev(kw)
+    o, lse = cdr.latent_attn_fwd(**d, scale=scale)
+    grads = cdr.latent_attn_bwd(**d, o=o, lse=lse, do=do.to(DEV), scale=scale)
+    compare(kw, do, o, lse, grads, scale)
+    return (o, lse) + grads
+
+
+@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 257])
+def test_one_sequence(T):
+    run(*make([T], [T], 2, T, packed=False))
+
+
+@pytest.mark.parametrize("H", [1, 3, 8])
+def test_equal_lengths(H):
+    run(*make([70] * 3, [70] * 3, H, H, packed=False))
+    run(*make([40] * 2, [150] * 2, H, 10 + H, packed=False))        # a context of 110 keys
+
+
+@pytest.mark.parametrize("lq,lk", [
+    ((1, 130, 64, 3), (1, 130, 64, 3)), ((5, 0, 129, 0, 1), (5, 0, 129, 0, 1)),
+    ((1, 1, 1, 1), (300, 64, 1, 65)), ((10, 128, 33), (200, 129, 1000)), ((0, 4), (70, 4)),
+    ((64, 65), (0, 65)), ((200, 3), (100, 1)), ((130, 250), (129, 60)), ((1,) * 40, (2,) * 40)])
+def test_packed(lq, lk):
+    """Tails, empty sequences, contexts, rows without keys, keys that no row sees."""
+    run(*make(lq, lk, 2, sum(lq) + 3 * sum(lk)))
+
+
+def test_long_sequence():
+    run(*make([1500], [1500], 1, 21))
+    run(*make([700], [2100], 2, 22))
+
+
+def test_behind_the_last_sequence_is_left_alone():
+    kw, do = make([30, 41], [50, 41], 2, 23, spare=5)
+    d = dev(kw)
+    d["q"][:, 71:], d["k_rope"][:, 91:], d["v"][:, 91:] = math.nan, math.nan, math.inf   # no sequence's
+    d["k_nope"][:, 91:] = math.nan
+    out = torch.full((1, 76, 2, 128), 3.0, dtype=BF16, device=DEV)
+    lse = torch.full((1, 76, 2), 3.0, device=DEV)
+    cdr.latent_attn_fwd(**d, out=out, lse_out=lse)
+    assert (out[:, 71:] == 3).all() and (lse[:, 71:] == 3).all()
+    compare(kw, do, out, lse, None, 192 ** -0.5)
+    out[:, 71:], lse[:, 71:] = math.nan, math.nan
+    grads = cdr.latent_attn_bwd(**d, o=out, lse=lse, do=do.to(DEV))
+    compare(kw, do, out, lse, grads, 192 ** -0.5)
+
+
+def test_neighbours_of_a_sequence_do_not_matter():
+    """The same sequence between others that hold NaN, with the same bits."""
+    kw, do = make([77], [90], 2, 24)
+    alone = run(kw, do)
+    big, _ = make([64, 77, 50], [70, 90, 50], 2, 25)
+    d = dev(big)
+    ddo = torch.full((1, 191, 2, 128), math.nan, dtype=BF16, device=DEV)
+    for n in ("q", "k_nope", "k_rope", "v"):
+        a, b = (64, 141) if n == "q" else (70, 160)
+        d[n].fill_(math.nan)
+        d[n][:, a:b] = kw[n].to(DEV)
+    ddo[:, 64:141] = do.to(DEV)
+    o, lse = cdr.latent_attn_fwd(**d)
+    dq, dk, dkr, dv = cdr.latent_attn_bwd(**d, o=o, lse=lse, do=ddo)
+    for got, want in zip((o, lse, dq), (alone[0], alone[1], alone[2])):
+        assert torch.equal(got[:, 64:141], want)
+    for got, want in zip((dk, dkr, dv), alone[3:]):
+        assert torch.equal(got[:, 70:160], want)
+
+
+def test_layouts_give_the_same():
+    kw, do = make([60, 9], [60, 9], 3, 26)
+    want = run(kw, do)
+    dense = {k: v.contiguous().to(DEV) for k, v in kw.items()}
+    turned = dict(dense, q=dense["q"].permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3))
+    odd = torch.empty(69 * 3 * 128 + 1, dtype=BF16, device=DEV)[1:].view(1, 69, 3, 128)
+    odd.copy_(dense["v"])
+    for d in (dense, turned, dict(dense, v=odd), dict(dense, v=dense["v"].permute(0, 1, 3, 2).contiguous().permute(0, 1, 3, 2))):
+        o, lse = cdr.latent_attn_fwd(**d)
+        g = cdr.latent_attn_bwd(**d, o=o, lse=lse, do=do.to(DEV))
+        for a, b in zip((o, lse) + g, want):
+            assert torch.equal(a, b)
+
+
+def test_scales_and_large_scores():
+    kw, do = make([100], [130], 2, 27)
+    run(kw, do, scale=0.4)
+    kw["q"] = (kw["q"].float() * 20).to(BF16)
+    run(kw, do)
+
+
+def test_no_tokens():
+    kw, do = make([0], [0], 2, 28, packed=False)
+    d = dev(kw)
+    o, lse = cdr.latent_attn_fwd(**d)
+    assert o.shape == (1, 0, 2, 128) and lse.shape == (1, 0, 2)
+    assert all(g.numel() == 0 for g in cdr.latent_attn_bwd(**d, o=o, lse=lse, do=do.to(DEV)))
+    run(*make([3], [0], 2, 29, packed=False))
+    run(*make([0], [3], 2, 30, packed=False))
+
+
+def test_graph_replays():
+    kw, do = make([150, 40], [170, 40], 2, 31)
+    d, do = dev(kw), do.to(DEV)
+
+    def step():
+        o, lse = cdr.latent_attn_fwd(**d)
+        return (o, lse) + cdr.latent_attn_bwd(**d, o=o, lse=lse, do=do)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for seed, lq, lk in ((41, (150, 40), (170, 40)), (42, (10, 180), (10, 200)), (43, (190, 0), (200, 10))):
+        new, ndo = make(lq, lk, 2, seed)
+        for k, v in new.items():
+            d[k].copy_(v)
+        do.copy_(ndo)
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(new, ndo, held[0], held[1], held[2:], 192 ** -0.5)
+        for a, b in zip(held, step()):
+            assert torch.equal(a, b)
+
+
+def test_gradients_match_differences():
+    """Directional differences of the forward itself: o's change along the gradient's direction, in the
+    fp64 oracle's step, against the gradient's product with it."""
+    kw, do = make([90], [90], 2, 32)
+    _, _, dq, dk, dkr, dv = run(kw, do)
+    g = torch.Generator().manual_seed(33)
+    for name, grad in (("q", dq), ("k_nope", dk), ("k_rope", dkr), ("v", dv)):
+        u = torch.randn(kw[name].shape, generator=g, dtype=torch.float64)
+        step = 1e-5
+        loss = []
+        for s in (step, -step):
+            moved = {k: v.double() if v.is_floating_point() else v for k, v in kw.items()}
+            moved[name] = moved[name] + s * u
+            loss.append(float((oracle_latent.attention(**moved, scale=192 ** -0.5)["o"] * do.double()).sum()))
+        want = (loss[0] - loss[1]) / (2 * step)
+        got = float((grad.cpu().double() * u).sum())
+        # rounding of the gradient: at most 5 * 2^-8 of its absolute terms, of random sign
+        assert abs(got - want) <= 5 * 2.0 ** -8 * float((grad.cpu().double().square() * u.square()).sum().sqrt()) * 4
+
+
+def test_prefill_agrees_with_decode():
+    """The two forms of one layer: keys and values expanded from latents, and the query absorbed."""
+    g = torch.Generator().manual_seed(34)
+    H, T = 4, 70
+    c, r = torch.randn(T, 512, generator=g).to(BF16), torch.randn(T, 64, generator=g).to(BF16)
+    wk, wv = (torch.randn(H, 128, 512, generator=g) / 512 ** 0.5 for _ in range(2))
+    k = torch.einsum("hdc,tc->thd", wk, c.float()).to(BF16)
+    v = torch.einsum("hdc,tc->thd", wv, c.float()).to(BF16)
+    q = torch.randn(T, H, 192, generator=g).to(BF16)
+    o, lse = cdr.latent_attn_fwd(q[None].to(DEV), k[None].to(DEV), r[None].to(DEV), v[None].to(DEV))
+    qc = torch.einsum("thd,hdc->thc", q[:, :, :128].float(), wk).to(BF16)
+    cache = torch.zeros(5, 16, 576, dtype=BF16, device=DEV)
+    cdr.latent_cache_write(c.to(DEV), r.to(DEV), cache, torch.arange(T, dtype=torch.int32, device=DEV))
+    oc, lse2 = cdr.latent_decode_fwd(qc[None].to(DEV), q[None, :, :, 128:].to(DEV), cache,
+                                     torch.arange(5, dtype=torch.int32, device=DEV)[None],
+                                     torch.tensor([T], dtype=torch.int32, device=DEV), 192 ** -0.5)
+    back = torch.einsum("thc,hdc->thd", oc[0].cpu().float(), wv)
+    # bf16 roundings of k, v and the absorbed q (2^-9 each at random) move scores of size ~1 and weights alike
+    assert (lse.cpu() - lse2.cpu()).abs().max() < 0.05
+    assert (o[0].cpu().float() - back).abs().max() < 0.05

@@ -237,3 +237,101 @@ def test_latent_decode_binding_errors():
                       (ValueError, (b(3, 512), b(3, 64), b(3, 16, 576), i(3)))):
         with pytest.raises(bad):
             cdr.latent_cache_write(*args)
+
+
+def test_latent_attention_oracle_gradients_match_differences():
+    from oracle import latent
+    g = torch.Generator().manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    H, lq, lk = 2, (3, 2), (5, 2)
+    x = dict(q=r(1, 5, H, 192), k_nope=r(1, 7, H, 128), k_rope=r(1, 7, 64), v=r(1, 7, H, 128))
+    cu = dict(cu_seqlens=torch.tensor([0, 3, 5]), cu_seqlens_k=torch.tensor([0, 5, 7]))
+    do = r(1, 5, H, 128)
+    got = latent.attention(**x, **cu, scale=0.1, do=do)
+    step = 1e-6
+    for name, grad in (("q", "dq"), ("k_nope", "dk_nope"), ("k_rope", "dk_rope"), ("v", "dv")):
+        flat = x[name].reshape(-1)
+        for i in range(0, flat.numel(), flat.numel() // 23):
+            keep = float(flat[i])
+            loss = []
+            for v in (keep + step, keep - step):
+                flat[i] = v
+                loss.append(float((latent.attention(**x, **cu, scale=0.1)["o"] * do).sum()))
+            flat[i] = keep
+            assert abs((loss[0] - loss[1]) / (2 * step) - float(got[grad].reshape(-1)[i])) < 1e-7
+        assert (got[grad].abs() <= got[grad + "_mag"] + 1e-12).all()
+
+
+def test_latent_attention_oracle_rows_without_keys():
+    from oracle import latent
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    got = latent.attention(r(1, 4, 1, 192), r(1, 2, 1, 128), r(1, 2, 64), r(1, 2, 1, 128), 0.1, do=r(1, 4, 1, 128))
+    assert (got["o"][0, :2] == 0).all() and (got["lse"][0, :2] == float("-inf")).all()
+    assert (got["dq"][0, :2] == 0).all() and torch.isfinite(got["dk_rope"]).all()
+
+
+def test_latent_attn_struct_and_check():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(ops.__file__), "..", "include", "chunk_dr.h")).read()
+    body = re.search(r"typedef struct \{([^{}]*)\} cdr_latent_attn_problem;", text).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    fields = re.findall(r"(?:int32_t|int64_t|float)\s+(\w+)(?:\[2\])?;", body)
+    assert fields == [f[0] for f in ops.cdr_latent_attn_problem._fields_]
+    lib = cdr.load_library()
+    ok = dict(N=2, T=9, Tk=9, H=4, varlen=0, scale=0.1)
+
+    def problem(**kw):
+        p = ops.cdr_latent_attn_problem(*{**ok, **{k: v for k, v in kw.items() if k in ok}}.values())
+        for n, v in (("q_stride", (768, 192)), ("k_stride", (512, 128)), ("v_stride", (512, 128))):
+            getattr(p, n)[:] = kw.get(n, v)
+        p.k_rope_stride = kw.get("k_rope_stride", 64)
+        return p
+
+    for kw, status in ((dict(), 0), (dict(N=0), 2), (dict(T=-1), 2), (dict(Tk=-1), 2), (dict(H=0), 2),
+                       (dict(scale=0.0), 2), (dict(scale=-1.0), 2), (dict(scale=float("nan")), 2),
+                       (dict(scale=float("inf")), 2), (dict(H=40000), 3), (dict(T=2 ** 30), 2), (dict(Tk=2 ** 30), 2),
+                       (dict(T=0), 0), (dict(Tk=0), 0), (dict(q_stride=(768, 4)), 3), (dict(k_stride=(-8, 128)), 3),
+                       (dict(v_stride=(2 ** 23, 128)), 3), (dict(k_rope_stride=68), 3)):
+        assert lib.cdr_latent_attn_check(ctypes.byref(problem(**kw))) == status, kw
+    p = problem()
+    fake, big = 1 << 20, 1 << 40
+    args = [fake] * 4 + [None, None] + [fake, fake]
+    for i in (0, 1, 2, 3, 6, 7):
+        bad = list(args)
+        bad[i] = None
+        assert lib.cdr_latent_attn_fwd(ctypes.byref(p), *bad, None) == 1, i
+    bad = list(args)
+    bad[3] = fake + 8
+    assert lib.cdr_latent_attn_fwd(ctypes.byref(p), *bad, None) == 3
+    assert lib.cdr_latent_attn_fwd(ctypes.byref(problem(varlen=1)), *args, None) == 1
+    args = [fake] * 4 + [None, None] + [fake] * 7
+    for i in [0, 1, 2, 3] + list(range(6, 13)):
+        bad = list(args)
+        bad[i] = None
+        assert lib.cdr_latent_attn_bwd(ctypes.byref(p), *bad, fake, big, None) == 1, i
+    assert lib.cdr_latent_attn_bwd(ctypes.byref(p), *args, fake, 64, None) == 5
+    assert lib.cdr_latent_attn_bwd(ctypes.byref(p), *args, fake + 4, big, None) == 5
+
+
+def test_latent_attn_binding_errors():
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    good = dict(q=b(1, 5, 2, 192), k_nope=b(1, 5, 2, 128), k_rope=b(1, 5, 64), v=b(1, 5, 2, 128))
+    for bad, kw in ((ValueError, dict(q=b(1, 5, 2, 128))), (TypeError, dict(q=b(1, 5, 2, 192).float())),
+                    (ValueError, dict(k_nope=b(1, 5, 3, 128))), (ValueError, dict(k_rope=b(1, 4, 64))),
+                    (ValueError, dict(v=b(1, 5, 2, 64))), (ValueError, dict(cu_seqlens_k=i(2))),
+                    (ValueError, dict(cu_seqlens=i(2), cu_seqlens_k=i(3))), (TypeError, dict(cu_seqlens=i(2).long())),
+                    (ValueError, dict(cu_seqlens=i(2), q=b(1, 4, 2, 192))), (ValueError, dict(scale=-0.1)),
+                    (ValueError, dict(out=b(1, 5, 128, 2).transpose(2, 3))), (ValueError, dict())):
+        with pytest.raises(bad):
+            cdr.latent_attn_fwd(**{**good, **kw})
+    two = dict(q=b(2, 5, 2, 192), k_nope=b(2, 5, 2, 128), k_rope=b(2, 5, 64), v=b(2, 5, 2, 128), cu_seqlens=i(2))
+    with pytest.raises(ValueError):
+        cdr.latent_attn_fwd(**two)
+    o, lse = b(1, 5, 2, 128), torch.zeros(1, 5, 2)
+    for bad, kw in ((ValueError, dict(o=b(1, 5, 2, 64))), (TypeError, dict(lse=b(1, 5, 2))),
+                    (TypeError, dict(do=o.float())), (ValueError, dict())):
+        with pytest.raises(bad):
+            cdr.latent_attn_bwd(**{**good, "o": o, "lse": lse, "do": o, **kw})
