@@ -21,6 +21,7 @@
 // rounded once.  h is the norm of the fp32 r, not of the rounded one.
 #include "chunk_dr.h"
 #include "cdr_common.h"
+#include <type_traits>
 
 namespace cdr {
 
@@ -68,33 +69,52 @@ struct Row {
     static __device__ __forceinline__ int at(int lane, int e) {
         return VEC == 8 ? ((e >> 3) * G + lane) * 8 + (e & 7) : e * G + lane;
     }
+    // A thread's elements as loaded.  All of a row's operands are loaded before the first is
+    // unpacked: unpacked one by one inside the bounds check, each waited for the one before (the
+    // backward at 8192 x 2048 took 95 us, now 66).
     template <typename T>
-    static __device__ __forceinline__ void load(const T* p, int lane, int D, float (&f)[E]) {
-        if constexpr (VEC == 8) {
+    struct Raw {
+        static constexpr int N = VEC == 8 ? (sizeof(T) == 2 ? E / 8 : E / 4) : E;
+        typedef typename std::conditional<VEC == 8, uint4, T>::type Unit;
+        Unit v[N];
+        __device__ __forceinline__ void load(const T* p, int lane, int D) {
+            if constexpr (VEC == 8) {
+                constexpr int PER = sizeof(T) == 2 ? 1 : 2;   // 16-byte units of eight elements
 #pragma unroll
-            for (int c = 0; c < E / 8; ++c) {
-                const int i = (c * G + lane) * 8;
-                if (i < D) {
-                    if constexpr (sizeof(T) == 2) {
-                        unpack8(*reinterpret_cast<const uint4*>(p + i), f + 8 * c);
-                    } else {
-                        const float4 a = *reinterpret_cast<const float4*>(p + i);
-                        const float4 b = *reinterpret_cast<const float4*>(p + i + 4);
-                        f[8 * c] = a.x, f[8 * c + 1] = a.y, f[8 * c + 2] = a.z, f[8 * c + 3] = a.w;
-                        f[8 * c + 4] = b.x, f[8 * c + 5] = b.y, f[8 * c + 6] = b.z, f[8 * c + 7] = b.w;
-                    }
-                } else {
+                for (int c = 0; c < E / 8; ++c) {
+                    const int i = (c * G + lane) * 8;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[8 * c + e] = 0.f;
+                    for (int u = 0; u < PER; ++u)
+                        v[PER * c + u] = i < D ? reinterpret_cast<const uint4*>(p + i)[u] : make_uint4(0, 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int i = e * G + lane;
+                    v[e] = i < D ? p[i] : T(0);
                 }
             }
-        } else {
+        }
+        __device__ __forceinline__ void get(float (&f)[E]) const {
+            if constexpr (VEC == 8 && sizeof(T) == 2) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int i = e * G + lane;
-                f[e] = i < D ? Elem<T>::get(p[i]) : 0.f;
+                for (int c = 0; c < N; ++c) unpack8(v[c], f + 8 * c);
+            } else if constexpr (VEC == 8) {
+#pragma unroll
+                for (int c = 0; c < N; ++c) {
+                    f[4 * c] = __uint_as_float(v[c].x), f[4 * c + 1] = __uint_as_float(v[c].y);
+                    f[4 * c + 2] = __uint_as_float(v[c].z), f[4 * c + 3] = __uint_as_float(v[c].w);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) f[e] = Elem<T>::get(v[e]);
             }
         }
+    };
+    static __device__ __forceinline__ void load(const float* p, int lane, int D, float (&f)[E]) {
+        Raw<float> r;
+        r.load(p, lane, D);
+        r.get(f);
     }
     template <typename T>
     static __device__ __forceinline__ void store(T* p, int lane, int D, const float (&f)[E]) {
@@ -169,16 +189,21 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_fwd_kernel(NormArgs a)
     if (a.w) R::load(a.w, lane, D, w);
     if (a.s) R::load(a.s, lane, D, s);
     if (a.w2) R::load(a.w2, lane, D, w2);
-    // every thread of a workgroup takes the same number of turns (row_sums holds a barrier); rows
-    // past the end are computed from row 0 and not stored
+    // Every thread of a workgroup takes the same number of turns (row_sums holds a barrier); rows
+    // past the end are computed from row 0 and not stored.
     for (int64_t base = (int64_t)blockIdx.x * RPW; base < a.rows; base += (int64_t)gridDim.x * RPW) {
         const int64_t at = base + threadIdx.x / G;
         const bool live = at < a.rows;
         const int row = live ? (int)at : 0;
         float n[E], z[E], x[E];
-        R::load(row_at<TA>(a.y, row, a.inner, a.yo, a.yi), lane, D, n);
-        if (a.z) R::load(row_at<TA>(a.z, row, a.inner, a.zo, a.zi), lane, D, z);
-        if (a.x) R::load(row_at<TR>(a.x, row, a.inner, a.xo, a.xi), lane, D, x);
+        typename R::template Raw<TA> ly, lz;
+        typename R::template Raw<TR> lx;
+        ly.load(row_at<TA>(a.y, row, a.inner, a.yo, a.yi), lane, D);
+        if (a.z) lz.load(row_at<TA>(a.z, row, a.inner, a.zo, a.zi), lane, D);
+        if (a.x) lx.load(row_at<TR>(a.x, row, a.inner, a.xo, a.xi), lane, D);
+        ly.get(n);
+        if (a.z) lz.get(z);
+        if (a.x) lx.get(x);
         float k = a.alpha;
         if (a.w) {
             float q[1] = {0.f};
@@ -233,6 +258,7 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_bwd_kernel(NormArgs a)
     if (a.w) R::load(a.w, lane, D, w);
     if (a.s) R::load(a.s, lane, D, s);
     if (a.w2) R::load(a.w2, lane, D, w2);
+    const bool silu = a.z && a.act == CDR_ACT_SILU;
     float cw[E], cs[E], cw2[E];   // column sums of the rows that this thread's group takes
 #pragma unroll
     for (int e = 0; e < E; ++e) cw[e] = cs[e] = cw2[e] = 0.f;
@@ -240,15 +266,23 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_bwd_kernel(NormArgs a)
         const int64_t at = base + threadIdx.x / G;
         const bool live = at < a.rows;
         const int row = live ? (int)at : 0;
-        float y[E], z[E], x[E], d[E];
-        R::load(row_at<TA>(a.y, row, a.inner, a.yo, a.yi), lane, D, y);
-        if (a.z) R::load(row_at<TA>(a.z, row, a.inner, a.zo, a.zi), lane, D, z);
-        if (a.x && a.w2) R::load(row_at<TR>(a.x, row, a.inner, a.xo, a.xi), lane, D, x);
-        if (a.dr && live) {
-            R::load(static_cast<const TR*>(a.dr) + (size_t)row * D, lane, D, d);
-        } else {
+        float y[E], z[E], x[E], d[E], dh[E];
+        typename R::template Raw<TA> ly, lz, lh;
+        typename R::template Raw<TR> lx, ld;
+        ly.load(row_at<TA>(a.y, row, a.inner, a.yo, a.yi), lane, D);
+        if (a.z) lz.load(row_at<TA>(a.z, row, a.inner, a.zo, a.zi), lane, D);
+        if (a.x && a.w2) lx.load(row_at<TR>(a.x, row, a.inner, a.xo, a.xi), lane, D);
+        if (a.dr) ld.load(static_cast<const TR*>(a.dr) + (size_t)row * D, lane, D);
+        if (a.w2) lh.load(static_cast<const TA*>(a.dh) + (size_t)row * D, lane, D);
+        ly.get(y);
+        if (a.z) lz.get(z);
+        if (a.x && a.w2) lx.get(x);
+        if (a.dr) ld.get(d);
+        if (a.w2) lh.get(dh);
 #pragma unroll
-            for (int e = 0; e < E; ++e) d[e] = 0.f;
+        for (int e = 0; e < E; ++e) {   // rows past the end have no gradients
+            d[e] = a.dr && live ? d[e] : 0.f;
+            dh[e] = a.w2 && live ? dh[e] : 0.f;
         }
         float ry = 1.f;
         if (a.w) {
@@ -258,22 +292,23 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_bwd_kernel(NormArgs a)
             row_sums<G, 1>(q, red, turn);
             ry = rsqrtf(q[0] * a.inv_d + a.eps);
         }
+        // y^ from here on, and the gate's sigmoid
+        float sg[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            y[e] *= ry;
+            sg[e] = a.z ? sigmoid(z[e]) : 1.f;
+        }
         if (a.w2) {
             // r again, then d += rstd(r) c(r, dh w2)
-            float r[E], dh[E];
-            if (live) {
-                R::load(static_cast<const TA*>(a.dh) + (size_t)row * D, lane, D, dh);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) dh[e] = 0.f;
-            }
+            float r[E];
             float q[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                float t = a.alpha * ry * y[e];
+                float t = a.alpha * y[e] * sg[e];
                 if (a.w) t *= w[e];
                 if (a.s) t *= s[e];
-                if (a.z) t *= (a.act == CDR_ACT_SILU ? z[e] : 1.f) * sigmoid(z[e]);
+                if (silu) t *= z[e];
                 if (a.x) t += x[e];
                 r[e] = t;
                 q[0] += t * t;
@@ -294,30 +329,27 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_bwd_kernel(NormArgs a)
         float q[1] = {0.f};
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            float g = 1.f, slope = 0.f;
-            if (a.z) {
-                const float sg = sigmoid(z[e]);
-                g = a.act == CDR_ACT_SILU ? z[e] * sg : sg;
-                slope = a.act == CDR_ACT_SILU ? sg * (1.f + z[e] * (1.f - sg)) : sg * (1.f - sg);
-            }
-            const float hat = ry * y[e];
-            const float n = a.w ? hat * w[e] : hat;
+            const float g = silu ? z[e] * sg[e] : sg[e];
+            const float slope = sg[e] * (silu ? 1.f + z[e] * (1.f - sg[e]) : 1.f - sg[e]);
+            const float n = a.w ? y[e] * w[e] : y[e];
             const float da = a.alpha * d[e];
-            cs[e] += da * g * n;
+            if (a.s) cs[e] += da * g * n;
             const float ds = a.s ? da * s[e] : da;
-            z[e] = ds * n * slope;
+            if (a.z) z[e] = ds * n * slope;
             float p = ds * g;
-            cw[e] += p * hat;
-            if (a.w) p *= w[e];
+            if (a.w) {
+                cw[e] += p * y[e];
+                p *= w[e];
+                q[0] += p * y[e];
+            }
             d[e] = p;
-            q[0] += p * hat;
         }
         if (a.dz && live) R::store(static_cast<TA*>(a.dz) + (size_t)row * D, lane, D, z);
         if (a.w) {
             row_sums<G, 1>(q, red, turn);
             const float m = q[0] * a.inv_d;
 #pragma unroll
-            for (int e = 0; e < E; ++e) d[e] = ry * (d[e] - ry * y[e] * m);
+            for (int e = 0; e < E; ++e) d[e] = ry * (d[e] - y[e] * m);
         }
         if (live) R::store(static_cast<TA*>(a.h) + (size_t)row * D, lane, D, d);
     }
@@ -349,20 +381,26 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_bwd_kernel(NormArgs a)
     }
 }
 
-// Column sums of the partial rows: 64 columns a workgroup, four threads a column that each add every
-// fourth partial row, their four sums added in order.  blockIdx.y names the vector.
-__global__ __launch_bounds__(256) void norm_cols_kernel(const float* part, int parts, int D, float* dw, float* ds,
-                                                        float* dw2) {
+// Column sums of the partial rows: 64 columns a workgroup, sixteen threads a column that each add every
+// sixteenth partial row, their sums added in order.  blockIdx.y names the vector.  (With four threads
+// a column the chain of dependent loads took 38 us at 2048 columns, as long as the data's own pass.)
+__global__ __launch_bounds__(1024) void norm_cols_kernel(const float* part, int parts, int D, float* dw, float* ds,
+                                                         float* dw2) {
     float* out = blockIdx.y == 0 ? dw : blockIdx.y == 1 ? ds : dw2;
     if (out == nullptr) return;
-    __shared__ float sums[4][64];
+    __shared__ float sums[16][64];
     const int c = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6;
     float t = 0.f;
     if (c < D)
-        for (int i = k; i < parts; i += 4) t += part[((size_t)i * 3 + blockIdx.y) * D + c];
+#pragma unroll 8
+        for (int i = k; i < parts; i += 16) t += part[((size_t)i * 3 + blockIdx.y) * D + c];
     sums[k][threadIdx.x & 63] = t;
     __syncthreads();
-    if (k == 0 && c < D) out[c] = (sums[0][c & 63] + sums[1][c & 63]) + (sums[2][c & 63] + sums[3][c & 63]);
+    if (k == 0 && c < D) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) t += sums[i][c & 63];
+        out[c] = t;
+    }
 }
 
 int64_t bwd_parts(const cdr_block_norm_problem* p) {
@@ -515,7 +553,7 @@ cdr_status cdr_block_norm_bwd(const cdr_block_norm_problem* p, const void* y, co
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
     }
     if (p->has_weight || p->has_scale || p->has_next) {
-        hipLaunchKernelGGL(cdr::norm_cols_kernel, dim3((unsigned)((p->D + 63) / 64), 3), dim3(256), 0, s, part, (int)parts,
+        hipLaunchKernelGGL(cdr::norm_cols_kernel, dim3((unsigned)((p->D + 63) / 64), 3), dim3(1024), 0, s, part, (int)parts,
                            p->D, p->has_weight ? dweight : nullptr, p->has_scale ? dres_scale : nullptr,
                            p->has_next ? dnext_weight : nullptr);
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;

@@ -9,7 +9,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import ops
-from .blocks import _gpu, _on, _ptr
+from .blocks import _launch, _need_gpu, _on, _ptr
 from .ops import CDR_OK, _need, _raise, load_library
 
 LATENT_DIM, LATENT_ROPE = 512, 64
@@ -59,15 +59,12 @@ def latent_cache_write(c: torch.Tensor, k_rope: torch.Tensor, cache: torch.Tenso
     P, page = _check_cache(cache)
     device = cache.device
     _on(device, c=c, k_rope=k_rope, slot_map=slot_map)
-    stream, current = _gpu(device)
+    _need_gpu(device)
     c = _part(c.reshape(T, LATENT_DIM), "c", (T, LATENT_DIM))
     k_rope = _part(k_rope.reshape(T, LATENT_ROPE), "k_rope", (T, LATENT_ROPE))
     slot_map = slot_map.contiguous()
-    with current:
-        st = lib.cdr_latent_cache_write(T, P, page, _ptr(c), _ptr(k_rope), c.stride(0), k_rope.stride(0), _ptr(cache),
-                                        _ptr(slot_map), stream)
-    if st != CDR_OK:
-        _raise(st, "latent_cache_write")
+    _launch(device, "latent_cache_write", lib.cdr_latent_cache_write, T, P, page, _ptr(c), _ptr(k_rope), c.stride(0),
+            k_rope.stride(0), _ptr(cache), _ptr(slot_map))
 
 
 def _check_cache(cache):
@@ -143,7 +140,7 @@ def latent_decode_fwd(q_latent: torch.Tensor, q_rope: torch.Tensor, cache: torch
     st = lib.cdr_latent_decode_check(ref)
     if st != CDR_OK:
         _raise(st, "latent_decode_fwd")
-    stream, current = _gpu(device)
+    _need_gpu(device)
     need = lib.cdr_latent_decode_workspace_bytes(ref)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
@@ -157,12 +154,9 @@ def latent_decode_fwd(q_latent: torch.Tensor, q_rope: torch.Tensor, cache: torch
         lse_out = torch.empty((B, T, H), dtype=torch.float32, device=device)
     block_table, seq_lens = block_table.contiguous(), seq_lens.contiguous()
     cu = None if cu_seqlens is None else cu_seqlens.contiguous()
-    with current:
-        st = lib.cdr_latent_decode_fwd(ref, _ptr(qc), _ptr(qr), _ptr(cache), _ptr(block_table), _ptr(seq_lens),
-                                       _ptr(cu), _ptr(out), _ptr(lse_out), _ptr(workspace),
-                                       workspace.numel() * workspace.element_size(), stream)
-    if st != CDR_OK:
-        _raise(st, "latent_decode_fwd")
+    _launch(device, "latent_decode_fwd", lib.cdr_latent_decode_fwd, ref, _ptr(qc), _ptr(qr), _ptr(cache),
+            _ptr(block_table), _ptr(seq_lens), _ptr(cu), _ptr(out), _ptr(lse_out), _ptr(workspace),
+            workspace.numel() * workspace.element_size())
     return out, lse_out
 
 
@@ -247,15 +241,13 @@ def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor,
     if lse_out is not None:
         _need(lse_out, "lse_out", torch.float32, (c.B, c.T, c.H), dense=True)
     _on(c.device, out=out, lse_out=lse_out)
-    stream, current = _gpu(c.device)
+    _need_gpu(c.device)
     if out is None:
         out = torch.empty((c.B, c.T, c.H, VALUE_DIM), dtype=torch.bfloat16, device=c.device)
     if lse_out is None:
         lse_out = torch.empty((c.B, c.T, c.H), dtype=torch.float32, device=c.device)
-    with current:
-        st = c.lib.cdr_latent_attn_fwd(ctypes.byref(c.p), *c.inputs, _ptr(out), _ptr(lse_out), stream)
-    if st != CDR_OK:
-        _raise(st, "latent_attn_fwd")
+    _launch(c.device, "latent_attn_fwd", c.lib.cdr_latent_attn_fwd, ctypes.byref(c.p), *c.inputs, _ptr(out),
+            _ptr(lse_out))
     return out, lse_out
 
 
@@ -276,7 +268,7 @@ def latent_attn_bwd(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor,
     _need(do, "do", torch.bfloat16, shape)
     _need(lse, "lse", torch.float32, shape[:3])
     _on(c.device, o=o, do=do, lse=lse, workspace=workspace)
-    stream, current = _gpu(c.device)
+    _need_gpu(c.device)
     o, lse, do = ops._aligned(o), lse.contiguous(), ops._aligned(do)
     need = c.lib.cdr_latent_attn_bwd_workspace_bytes(ctypes.byref(c.p))
     if workspace is None:
@@ -289,10 +281,7 @@ def latent_attn_bwd(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor,
     dq = empty(c.B, c.T, c.H, QUERY_DIM)
     dk, dv = empty(c.B, c.Tk, c.H, NOPE_DIM), empty(c.B, c.Tk, c.H, VALUE_DIM)
     dkr = empty(c.B, c.Tk, LATENT_ROPE)
-    with current:
-        st = c.lib.cdr_latent_attn_bwd(ctypes.byref(c.p), *c.inputs, _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk),
-                                       _ptr(dkr), _ptr(dv), _ptr(workspace),
-                                       workspace.numel() * workspace.element_size(), stream)
-    if st != CDR_OK:
-        _raise(st, "latent_attn_bwd")
+    _launch(c.device, "latent_attn_bwd", c.lib.cdr_latent_attn_bwd, ctypes.byref(c.p), *c.inputs, _ptr(o), _ptr(lse),
+            _ptr(do), _ptr(dq), _ptr(dk), _ptr(dkr), _ptr(dv), _ptr(workspace),
+            workspace.numel() * workspace.element_size())
     return dq, dk, dkr, dv
