@@ -24,7 +24,17 @@ __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
-__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Waits for this wave's copies and loads.  The builtin, not asm: the compiler then knows that its own
+// earlier loads have arrived and does not wait for them again behind copies that are still under way.
+__device__ __forceinline__ void dma_wait() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+    asm volatile("" ::: "memory");
+}
+
+// Nothing is moved across this.  Between a batch of LDS reads and the products of the batch before
+// it: left alone, the compiler reads one operand, waits and multiplies, one LDS latency a product.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // Byte offset of an LDS pointer, as m0 and the asm above take it.
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {

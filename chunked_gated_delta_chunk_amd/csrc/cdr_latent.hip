@@ -10,21 +10,22 @@
 // product: 2 (576 + 512) flops a key and row against 1152 bytes a key.  With 16 rows the cache's
 // bytes bound it, with 128 the matrix rate is as near.
 //
-// A workgroup of four waves (eight for M = 64) takes M = 16, 32 or 64 rows and walks over tiles of
+// A workgroup of four waves (eight for M > 16) takes M = 16, 32 or 64 rows and walks over tiles of
 // 64 keys.
 //  - A tile (72 KiB) goes to LDS once, two deep, by 16-byte copies that need no registers; a key's
 //    latent row is one wave's copy, so its page is looked up in scalar registers.  16-byte pieces
 //    are stored at position p ^ (key & 15), which spreads both reads below over the banks.
-//  - Scores: a wave takes 16 keys against all M rows (half of them at M = 64); the rows' q stays in
-//    registers as the right operand, so the result S^T has a row of q in each lane and the running
-//    maximum is a lane's own value after two shuffles and one exchange between the waves.
+//  - Scores: a wave takes 16 or 32 keys against 16 rows, whose q stays in registers as the right
+//    operand, so the result S^T has a row of q in each lane and the running maximum is a lane's own
+//    value after two shuffles and one exchange between the waves.
 //  - Values: a wave takes its share of the 512 columns, O^T += V^T P^T, V^T through the transposing
 //    read; P^T goes through LDS in the operand's order.  So the tile is read from LDS once or twice
 //    a product and not once for every 16 rows, which would be the bound.
 //
 // Work is cut evenly over the device whatever the lengths: the tiles of all (sequence, row block)
-// units are numbered and each workgroup takes an equal run of them.  A unit that one workgroup
-// covers is written directly; a unit cut between workgroups leaves partial sums (fp32, with their
+// units are numbered and each workgroup takes an equal run of them.  Where a sequence has several row
+// blocks, a team of neighbouring workgroups takes them side by side, one block each, so that they
+// read the same keys at the same time through one L2.  A unit that one workgroup covers is written directly; a unit cut between workgroups leaves partial sums (fp32, with their
 // maximum and sum) that a second kernel joins in order.  The cut depends on the lengths and sizes
 // alone, so the same inputs give the same bits.
 #include "chunk_dr.h"
@@ -36,6 +37,7 @@ namespace {
 
 constexpr int DEC_GRID = 256;        // workgroups; LDS holds one on a CU
 constexpr int DEC_KEYS = 64;         // keys of a tile
+constexpr int DEC_TEAM = 8;          // most row blocks that are taken side by side
 
 struct LatentDecodeArgs {
     const uint16_t* qc;
@@ -48,9 +50,10 @@ struct LatentDecodeArgs {
     float* lse;
     float* part;       // [2 grid][M][512] partial sums
     float2* part_ml;   // [2 grid][M] their maximum (base 2) and sum
-    int4* rec;         // [grid] (n, row block, last workgroup) of the unit cut at this workgroup's end
+    int4* rec;         // [grid] (n, row block, parts) of the unit cut at this workgroup's end
     int64_t qct, qch, qrt, qrh;
     int N, T, H, cols, num_pages, shift;
+    int team;          // workgroups that take the row blocks of one sequence side by side
     float scale2;      // scale * log2(e)
 };
 
@@ -76,43 +79,55 @@ __device__ __forceinline__ SeqInfo dec_seq(const LatentDecodeArgs& a, int n) {
 __device__ __forceinline__ int dec_tiles(const SeqInfo& s) { return max((s.len + DEC_KEYS - 1) / DEC_KEYS, 1); }
 
 template <int M>
-__device__ __forceinline__ int dec_blocks(const SeqInfo& s, int H) {
-    return (int)(((int64_t)s.tokens * H + M - 1) / M);
+__device__ __forceinline__ int dec_blocks(const LatentDecodeArgs& a, const SeqInfo& s) {
+    return (int)(((int64_t)s.tokens * a.H + M - 1) / M);
+}
+// units of a sequence: its row blocks in teams
+template <int M>
+__device__ __forceinline__ int dec_units(const LatentDecodeArgs& a, const SeqInfo& s) {
+    return (dec_blocks<M>(a, s) + a.team - 1) / a.team;
 }
 
-// Cache row of key `key` of sequence n, or -1 where there is none.
-__device__ __forceinline__ int dec_row(const LatentDecodeArgs& a, int n, int len, int key) {
-    if (key >= len) return -1;
-    const int page = a.table[(size_t)n * a.cols + (key >> a.shift)];
+// The page of key `key` of sequence n, -1 behind its end; and that key's cache row, -1 where there is
+// none.  Apart, so that a page is loaded two tiles before its row is worked out.
+__device__ __forceinline__ int dec_page(const LatentDecodeArgs& a, int n, int len, int key) {
+    return key < len ? a.table[(size_t)n * a.cols + (key >> a.shift)] : -1;
+}
+__device__ __forceinline__ int dec_row(const LatentDecodeArgs& a, int page, int key) {
     if (page < 0 || page >= a.num_pages) return -1;
     return (page << a.shift) + (key & ((1 << a.shift) - 1));
 }
 
-template <int MT, int NW>
+template <int MT, int NW, int KG>
 __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeArgs a) {
     constexpr int M = 16 * MT;
-    constexpr int RH = NW / 4, MQ = MT / RH;   // row parts of the scores, row tiles of a wave there
+    constexpr int KT = 4 / KG;                 // scores: key groups KG, 16-key tiles of a wave,
+    constexpr int RH = NW / KG, MQ = MT / RH;  // row parts, row tiles of a wave
     constexpr int CT = 32 / NW;                // 16-column tiles of a wave in the values' product
     constexpr int KPW = DEC_KEYS / NW;         // keys of a tile that a wave copies
     constexpr int DEC_THREADS = 64 * NW;
     __shared__ __align__(256) char kc[2][DEC_KEYS * LC * 2];
     __shared__ __align__(256) char kr[2][DEC_KEYS * LR * 2];
     __shared__ __align__(16) char pf[MT * 2 * 1024];   // P^T in operand order
-    __shared__ float mx[4][M];
+    __shared__ float mx[KG][M];
     __shared__ int64_t scan[NW];
     __shared__ int64_t found[2];
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, q = lane >> 4;
-    const int kg = w & 3, rh = w >> 2;         // the wave's keys and row part in the scores
-    const int wg = blockIdx.x;
+    const int kg = w % KG, rh = w / KG;        // the wave's keys and row part in the scores
+    // workgroups go round the 8 XCDs: numbered so that neighbours, which read the same sequence, share an L2
+    const int wg = (blockIdx.x & 7) * (DEC_GRID / 8) + (blockIdx.x >> 3);
 
     // total tiles, then the sequence in which this workgroup's run begins
-    int64_t total = 0;
-    for (int n = tid; n < a.N; n += DEC_THREADS) {
+    auto tiles_of = [&](int n) {
+        if (n >= a.N) return (int64_t)0;
         const SeqInfo s = dec_seq(a, n);
-        total += (int64_t)dec_blocks<M>(s, a.H) * dec_tiles(s);
-    }
+        return (int64_t)dec_units<M>(a, s) * dec_tiles(s);
+    };
+    const int64_t first = tiles_of(tid);
+    int64_t total = first;
+    for (int n = tid + DEC_THREADS; n < a.N; n += DEC_THREADS) total += tiles_of(n);
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) total += __shfl_xor(total, m, 64);
     if (lane == 0) scan[w] = total;
@@ -121,18 +136,15 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
 #pragma unroll
     for (int i = 0; i < NW; ++i) total += scan[i];
     __syncthreads();
-    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t begin = wg * share, end = min(total, begin + share);
+    const int teams = DEC_GRID / a.team, team = wg / a.team, member = wg - team * a.team;
+    const int64_t share = (total + teams - 1) / teams;
+    const int64_t begin = team * share, end = min(total, begin + share);
     if (tid == 0) a.rec[wg] = make_int4(-1, 0, 0, 0);
-    if (begin >= end) return;
+    if (begin >= end || team >= teams) return;
     int64_t before = 0;
     for (int base = 0; base < a.N; base += DEC_THREADS) {
         const int n = base + tid;
-        int64_t own = 0;
-        if (n < a.N) {
-            const SeqInfo s = dec_seq(a, n);
-            own = (int64_t)dec_blocks<M>(s, a.H) * dec_tiles(s);
-        }
+        const int64_t own = base == 0 ? first : tiles_of(n);
         int64_t sum = own;
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
@@ -159,29 +171,34 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
     int64_t pos = begin;
 
     const uint32_t kc0 = lds_offset(kc), kr0 = lds_offset(kr);
-    // where this lane reads in a tile: key 16 kg + r, pieces 4 k + q (the exclusive or leaves bits 4
+    // where this lane reads in a tile: key 16 KT kg + r, pieces 4 k + q (the exclusive or leaves bits 4
     // and up of the piece alone, so four bases and fixed steps serve all k), the rope pieces, and for
     // the transposed reads key 4 q + r / 4, the 8 bytes 4 (r & 3) .. of each column tile
     int k_at[4], r_at[2], v_at[CT];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) k_at[k] = (16 * kg + r) * (LC * 2) + ((4 * k + q) ^ r) * 16;
+    for (int k = 0; k < 4; ++k) k_at[k] = (16 * KT * kg + r) * (LC * 2) + ((4 * k + q) ^ r) * 16;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) r_at[k] = (16 * kg + r) * (LR * 2) + ((4 * k + q) ^ ((r >> 1) & 7)) * 16;
+    for (int k = 0; k < 2; ++k) r_at[k] = (16 * KT * kg + r) * (LR * 2) + ((4 * k + q) ^ ((r >> 1) & 7)) * 16;
 #pragma unroll
     for (int c = 0; c < CT; ++c)
         v_at[c] = (4 * q + (r >> 2)) * (LC * 2) + ((2 * (CT * w + c) + ((r >> 1) & 1)) ^ (4 * q + (r >> 2))) * 16 +
                   (r & 1) * 8;
     while (pos < end) {
         const SeqInfo s = dec_seq(a, n);
-        const int tiles = dec_tiles(s), blocks = dec_blocks<M>(s, a.H);
-        if (pos >= unit0 + (int64_t)blocks * tiles) {
-            unit0 += (int64_t)blocks * tiles;
+        const int tiles = dec_tiles(s), units = dec_units<M>(a, s);
+        if (pos >= unit0 + (int64_t)units * tiles) {
+            unit0 += (int64_t)units * tiles;
             ++n;
             continue;
         }
-        const int rb = (int)((pos - unit0) / tiles);
-        const int t0 = (int)((pos - unit0) - (int64_t)rb * tiles);
+        const int unit = (int)((pos - unit0) / tiles);
+        const int t0 = (int)((pos - unit0) - (int64_t)unit * tiles);
         const int t1 = (int)min((int64_t)tiles, t0 + (end - pos));
+        const int rb = unit * a.team + member;
+        if (rb >= dec_blocks<M>(a, s)) {   // the last team of a sequence may be short
+            pos += t1 - t0;
+            continue;
+        }
         const int64_t rows = (int64_t)s.tokens * a.H;
 
         // ---- q of this block's rows, and each row's key limit
@@ -234,43 +251,72 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
             }
         };
 
-        int row = dec_row(a, n, s.len, 64 * t0 + lane);
+        const int page0 = dec_page(a, n, s.len, 64 * t0 + lane);
+        int page = dec_page(a, n, s.len, 64 * (t0 + 1) + lane);   // of the next tile
+        dma_wait();        // q and the pages are there
         __syncthreads();   // the previous block's reads of LDS have ended
+        int row = dec_row(a, page0, 64 * t0 + lane);
         load_tile(0, row);
         for (int j = t0; j < t1; ++j) {
             const int buf = (j - t0) & 1;
             const uint64_t there = __ballot(row >= 0);
-            const int next = j + 1 < t1 ? dec_row(a, n, s.len, 64 * (j + 1) + lane) : -1;
             dma_wait();
             __syncthreads();
-            if (j + 1 < t1) load_tile(buf ^ 1, next);
-            row = next;
+            row = dec_row(a, page, 64 * (j + 1) + lane);
+            page = dec_page(a, n, s.len, 64 * (j + 2) + lane);
+            if (j + 1 < t1) load_tile(buf ^ 1, row);
 
-            // ---- S^T of this wave's 16 keys and row part
-            f32x4 sc[MQ];
+            // ---- S^T of this wave's keys and row part
+            f32x4 sc[KT][MQ];
 #pragma unroll
-            for (int mt = 0; mt < MQ; ++mt) sc[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int mt = 0; mt < MQ; ++mt) sc[kt][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
             const char* kw = kc[buf];
             const char* rw = kr[buf];
+            // a few of the eighteen steps at a time, the next few's keys read ahead
+            constexpr int STEPS = KT == 2 ? 2 : 3;
+            bf16x8 f[2][STEPS][KT];
+            auto read_keys = [&](int batch) {
 #pragma unroll
-            for (int k = 0; k < 18; ++k) {
-                const bf16x8 f = k < 16 ? lds16(kw + k_at[k & 3] + (k >> 2) * 256) : lds16(rw + r_at[k - 16]);
+                for (int i = 0; i < STEPS; ++i)
 #pragma unroll
-                for (int mt = 0; mt < MQ; ++mt) sc[mt] = mfma32(f, qf[mt][k], sc[mt]);
+                    for (int kt = 0; kt < KT; ++kt) {
+                        const int k = STEPS * batch + i;
+                        f[batch & 1][i][kt] = k < 16 ? lds16(kw + k_at[k & 3] + (k >> 2) * 256 + kt * 16 * (LC * 2))
+                                                     : lds16(rw + r_at[k - 16] + kt * 16 * (LR * 2));
+                    }
+            };
+            read_keys(0);
+#pragma unroll
+            for (int batch = 0; batch < 18 / STEPS; ++batch) {
+                if (batch < 18 / STEPS - 1) read_keys(batch + 1);
+                keep_order();
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                        for (int mt = 0; mt < MQ; ++mt)
+                            sc[kt][mt] = mfma32(f[batch & 1][i][kt], qf[mt][STEPS * batch + i], sc[kt][mt]);
+                keep_order();
             }
             const bool whole = there == ~0ull && 64 * j + 63 <= s.len - s.tokens;
 #pragma unroll
             for (int mt = 0; mt < MQ; ++mt) {
+                float t = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v = sc[mt][i] * a.scale2;
-                    if (!whole) {
-                        const int key = 16 * kg + 4 * q + i;
-                        if (64 * j + key >= lim[mt] || !((there >> key) & 1)) v = -INFINITY;
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v = sc[kt][mt][i] * a.scale2;
+                        if (!whole) {
+                            const int key = 16 * (KT * kg + kt) + 4 * q + i;
+                            if (64 * j + key >= lim[mt] || !((there >> key) & 1)) v = -INFINITY;
+                        }
+                        sc[kt][mt][i] = v;
+                        t = fmaxf(t, v);
                     }
-                    sc[mt][i] = v;
-                }
-                float t = fmaxf(fmaxf(sc[mt][0], sc[mt][1]), fmaxf(sc[mt][2], sc[mt][3]));
                 t = fmaxf(t, __shfl_xor(t, 16, 64));
                 t = fmaxf(t, __shfl_xor(t, 32, 64));
                 if (q == 0) mx[kg][16 * (rh * MQ + mt) + r] = t;
@@ -281,26 +327,34 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
             float alpha[MT];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const int i = 16 * mt + r;
-                const float t = fmaxf(fmaxf(mx[0][i], mx[1][i]), fmaxf(mx[2][i], mx[3][i]));
-                const float now = fmaxf(m[mt], t);
+                float now = m[mt];
+#pragma unroll
+                for (int g = 0; g < KG; ++g) now = fmaxf(now, mx[g][16 * mt + r]);
                 alpha[mt] = ex2(m[mt] - (now == -INFINITY ? 0.f : now));
                 same = same && alpha[mt] == 1.f;
                 m[mt] = now;
             }
 #pragma unroll
             for (int mt = 0; mt < MQ; ++mt) {
-                const float now = rh == 0 ? m[mt] : m[MT - MQ + mt];
-                const float ref = now == -INFINITY ? 0.f : now;
-                float p[4], sum = 0.f;
+                float now = m[mt], al = alpha[mt];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[e] = ex2(sc[mt][e] - ref);
-                    sum += p[e];
+                for (int h = 1; h < RH; ++h)
+                    if (rh == h) now = m[h * MQ + mt], al = alpha[h * MQ + mt];
+                const float ref = now == -INFINITY ? 0.f : now;
+                float sum = 0.f;
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = ex2(sc[kt][mt][e] - ref);
+                        sum += p[e];
+                    }
+                    const int tile = KT * kg + kt;
+                    *reinterpret_cast<uint2*>(&pf[((rh * MQ + mt) * 2 + (tile >> 1)) * 1024 + lane * 16 + (tile & 1) * 8]) =
+                        make_uint2(pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]));
                 }
-                l[mt] = l[mt] * (rh == 0 ? alpha[mt] : alpha[MT - MQ + mt]) + sum;
-                *reinterpret_cast<uint2*>(&pf[((rh * MQ + mt) * 2 + (kg >> 1)) * 1024 + lane * 16 + (kg & 1) * 8]) =
-                    make_uint2(pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]));
+                l[mt] = l[mt] * al + sum;
             }
             if (!__all(same)) {
 #pragma unroll
@@ -310,19 +364,32 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[mt][c][e] *= alpha[mt];
             }
-            lds_barrier();
-            // ---- O^T of this wave's columns
+            // ---- O^T of this wave's columns: the columns of the first 32 keys are read ahead of the
+            // barrier, those of the others during the first's products
+            bf16x8 v[2][CT], p[MT];
+            auto read_columns = [&](int t) {
+                const char* at = kc[buf] + t * 32 * (LC * 2);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                bf16x8 p[MT];
+                for (int c = 0; c < CT; ++c) v[t][c] = join8(lds_tr(at + v_at[c]), lds_tr(at + 16 * (LC * 2) + v_at[c]));
+            };
+            auto read_weights = [&](int t) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) p[mt] = lds16(&pf[(mt * 2 + t) * 1024 + lane * 16]);
-                const char* v = kc[buf] + t * 32 * (LC * 2);
+            };
+            read_columns(0);
+            lds_barrier();
+            read_weights(0);
+            read_columns(1);
+            keep_order();
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    const bf16x8 f = join8(lds_tr(v + v_at[c]), lds_tr(v + 16 * (LC * 2) + v_at[c]));
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) o[mt][c] = mfma32(f, p[mt], o[mt][c]);
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) o[mt][c] = mfma32(v[t][c], p[mt], o[mt][c]);
+                if (t == 0) {
+                    read_weights(1);
+                    keep_order();
                 }
             }
         }
@@ -341,7 +408,9 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int i = 16 * mt + r;
-            const float sum = (mx[0][i] + mx[1][i]) + (mx[2][i] + mx[3][i]);
+            float sum = mx[0][i];
+#pragma unroll
+            for (int g = 1; g < KG; ++g) sum += mx[g][i];
             const int64_t grow = (int64_t)rb * M + i;
             if (grow >= rows) continue;
             if (direct) {
@@ -361,18 +430,19 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
             }
         }
         if (t0 == 0 && t1 < tiles && tid == 0)
-            a.rec[wg] = make_int4(n, rb, (int)((pos + tiles - 1) / share), 0);
+            a.rec[wg] = make_int4(n, rb, (int)((pos + tiles - 1) / share) - team + 1, 0);
         pos += t1 - t0;
     }
 }
 
 // Joins the partial sums of a unit that was cut: workgroup (wg, row) takes one row of the unit that
-// began in workgroup wg's run, its four waves every fourth part each.
+// began in workgroup wg's run, its eight waves every eighth part each.
+constexpr int JOIN_WAVES = 8;
 template <int MT>
-__global__ __launch_bounds__(256) void latent_join_kernel(LatentDecodeArgs a) {
+__global__ __launch_bounds__(64 * JOIN_WAVES) void latent_join_kernel(LatentDecodeArgs a) {
     constexpr int M = 16 * MT;
-    __shared__ float sums[4][LC];
-    __shared__ float ml[4][2];
+    __shared__ float sums[JOIN_WAVES][LC];
+    __shared__ float ml[JOIN_WAVES][2];
     const int wg = blockIdx.x / M, i = blockIdx.x % M;
     const int4 rec = a.rec[wg];
     if (rec.x < 0) return;
@@ -380,14 +450,14 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentDecodeArgs a) {
     const int64_t grow = (int64_t)rec.y * M + i;
     if (grow >= (int64_t)s.tokens * a.H) return;
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int parts = rec.z - wg + 1;
+    const int parts = rec.z;
     float m = -INFINITY, l = 0.f;
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll 4
-    for (int k = w; k < parts; k += 4) {
-        const size_t slot = k == 0 ? 2 * wg + 1 : 2 * (size_t)(wg + k);
+    for (int k = w; k < parts; k += JOIN_WAVES) {
+        const size_t slot = k == 0 ? 2 * wg + 1 : 2 * (size_t)(wg + k * a.team);
         const float2 pm = a.part_ml[slot * M + i];
         const float4* p = reinterpret_cast<const float4*>(a.part + (slot * M + i) * LC) + 2 * lane;
         const float4 x = p[0], y = p[1];
@@ -409,24 +479,21 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentDecodeArgs a) {
     for (int e = 0; e < 8; ++e) sums[w][8 * lane + e] = acc[e];
     if (lane == 0) ml[w][0] = m, ml[w][1] = l;
     __syncthreads();
-    float top = -INFINITY, sum = 0.f, f[4];
+    float top = -INFINITY, sum = 0.f, v = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k][0]);
+    for (int k = 0; k < JOIN_WAVES; ++k) top = fmaxf(top, ml[k][0]);
     const float ref = top == -INFINITY ? 0.f : top;
+    const int c = threadIdx.x;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        f[k] = ex2(ml[k][0] - ref);
-        sum += ml[k][1] * f[k];
+    for (int k = 0; k < JOIN_WAVES; ++k) {
+        const float f = ex2(ml[k][0] - ref);
+        sum += ml[k][1] * f;
+        v += sums[k][c] * f;
     }
     const float inv = sum > 0.f ? 1.f / sum : sum;
     const size_t out = (size_t)s.bos * a.H + grow;
-    const int c = 2 * threadIdx.x;
-    float v[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-        v[e] = ((sums[0][c + e] * f[0] + sums[1][c + e] * f[1]) + (sums[2][c + e] * f[2] + sums[3][c + e] * f[3])) * inv;
-    *reinterpret_cast<uint32_t*>(a.o + out * LC + c) = pack_bf2(v[0], v[1]);
-    if (a.lse && threadIdx.x == 0) a.lse[out] = sum == 0.f ? -INFINITY : LN2 * (top + lg2(sum));
+    a.o[out * LC + c] = f2bf(v * inv);
+    if (a.lse && c == 0) a.lse[out] = sum == 0.f ? -INFINITY : LN2 * (top + lg2(sum));
 }
 
 // One wave a token: 64 16-byte pieces of the latent and 8 of the rope part into the cache row that
@@ -454,12 +521,12 @@ int dec_m(const cdr_latent_decode_problem* p) {
     return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-template <int MT, int NW>
+template <int MT, int NW, int KG>
 hipError_t launch_latent_decode(const LatentDecodeArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((latent_decode_kernel<MT, NW>), dim3(DEC_GRID), dim3(64 * NW), 0, s, a);
+    hipLaunchKernelGGL((latent_decode_kernel<MT, NW, KG>), dim3(DEC_GRID), dim3(64 * NW), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((latent_join_kernel<MT>), dim3(DEC_GRID * 16 * MT), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((latent_join_kernel<MT>), dim3(DEC_GRID * 16 * MT), dim3(64 * JOIN_WAVES), 0, s, a);
     return hipGetLastError();
 }
 
@@ -524,10 +591,13 @@ cdr_status cdr_latent_decode_fwd(const cdr_latent_decode_problem* p, const void*
     a.num_pages = p->num_pages;
     a.shift = __builtin_ctz((unsigned)p->page_size);
     a.scale2 = p->scale * cdr::LOG2E;
+    // packed batches have row blocks of no common number: each is a unit of its own
+    const int64_t blocks = ((int64_t)p->T * p->H + m - 1) / m;
+    a.team = p->varlen ? 1 : (int)(blocks < cdr::DEC_TEAM ? blocks : cdr::DEC_TEAM);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = m == 16   ? cdr::launch_latent_decode<1, 4>(a, s)
-                         : m == 32 ? cdr::launch_latent_decode<2, 4>(a, s)
-                                   : cdr::launch_latent_decode<4, 8>(a, s);
+    const hipError_t e = m == 16   ? cdr::launch_latent_decode<1, 4, 4>(a, s)
+                         : m == 32 ? cdr::launch_latent_decode<2, 8, 4>(a, s)
+                                   : cdr::launch_latent_decode<4, 8, 2>(a, s);
     return e == hipSuccess ? CDR_OK : CDR_ERR_HIP;
 }
 
