@@ -58,6 +58,30 @@ __device__ __forceinline__ bf16x8 lds16(const void* p) { return *static_cast<con
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
 
+// Where a tile's 16-byte pieces are stored: row `row` keeps piece p at p ^ f(row), f one to one on 16
+// rows.  f16 for rows of a multiple of 256 bytes, f8 for rows of 128 bytes (two of which share 256).
+__device__ __forceinline__ int f16(int row) { return ((row & 7) << 1) | ((row >> 3) & 1); }
+__device__ __forceinline__ int f8(int row) { return (((row >> 1) & 3) << 1) | ((row >> 3) & 1); }
+
+// 32x32x16 products: A[m = lane & 31][k = 8 (lane >> 5) + i], B likewise, and the result's register i
+// holds row 8 (i / 4) + 4 (lane >> 5) + i % 4 of column lane & 31.
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
+__device__ __forceinline__ f32x16 mma(const bf16x8& a, const bf16x8& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = 0.f;
+    return z;
+}
+// registers 8 t .. 8 t + 7 of a result as the right operand of the next product
+__device__ __forceinline__ bf16x8 operand(const f32x16& p, int t) {
+    const uint4 v = make_uint4(pack_bf2(p[8 * t], p[8 * t + 1]), pack_bf2(p[8 * t + 2], p[8 * t + 3]),
+                               pack_bf2(p[8 * t + 4], p[8 * t + 5]), pack_bf2(p[8 * t + 6], p[8 * t + 7]));
+    return __builtin_bit_cast(bf16x8, v);
+}
+
 // A value that the compiler computes where it is used: copies of a loop's fixed offsets for every
 // unrolled step, kept in registers over the loop, cost more than the one addition that makes them.
 __device__ __forceinline__ int fresh(int x) {

@@ -98,28 +98,19 @@ __device__ __forceinline__ int dec_row(const LatentDecodeArgs& a, int page, int 
     return (page << a.shift) + (key & ((1 << a.shift) - 1));
 }
 
-template <int MT, int NW, int KG>
-__global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeArgs a) {
-    constexpr int M = 16 * MT;
-    constexpr int KT = 4 / KG;                 // scores: key groups KG, 16-key tiles of a wave,
-    constexpr int RH = NW / KG, MQ = MT / RH;  // row parts, row tiles of a wave
-    constexpr int CT = 32 / NW;                // 16-column tiles of a wave in the values' product
-    constexpr int KPW = DEC_KEYS / NW;         // keys of a tile that a wave copies
-    constexpr int DEC_THREADS = 64 * NW;
-    __shared__ __align__(256) char kc[2][DEC_KEYS * LC * 2];
-    __shared__ __align__(256) char kr[2][DEC_KEYS * LR * 2];
-    __shared__ __align__(16) char pf[MT * 2 * 1024];   // P^T in operand order
-    __shared__ float mx[KG][M];
+// This workgroup's run of tiles: [begin, end) of all units' tiles, the sequence n in which it begins
+// and the number unit0 of that sequence's first tile.  False where there is nothing to do.
+struct Run {
+    int64_t begin, end, share, unit0;
+    int n, team, member;
+};
+
+template <int M, int THREADS>
+__device__ __forceinline__ bool dec_run(const LatentDecodeArgs& a, int wg, Run& run) {
+    constexpr int NW = THREADS / 64;
     __shared__ int64_t scan[NW];
     __shared__ int64_t found[2];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, q = lane >> 4;
-    const int kg = w % KG, rh = w / KG;        // the wave's keys and row part in the scores
-    // workgroups go round the 8 XCDs: numbered so that neighbours, which read the same sequence, share an L2
-    const int wg = (blockIdx.x & 7) * (DEC_GRID / 8) + (blockIdx.x >> 3);
-
-    // total tiles, then the sequence in which this workgroup's run begins
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     auto tiles_of = [&](int n) {
         if (n >= a.N) return (int64_t)0;
         const SeqInfo s = dec_seq(a, n);
@@ -127,7 +118,7 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
     };
     const int64_t first = tiles_of(tid);
     int64_t total = first;
-    for (int n = tid + DEC_THREADS; n < a.N; n += DEC_THREADS) total += tiles_of(n);
+    for (int n = tid + THREADS; n < a.N; n += THREADS) total += tiles_of(n);
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) total += __shfl_xor(total, m, 64);
     if (lane == 0) scan[w] = total;
@@ -136,15 +127,15 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
 #pragma unroll
     for (int i = 0; i < NW; ++i) total += scan[i];
     __syncthreads();
-    const int teams = DEC_GRID / a.team, team = wg / a.team, member = wg - team * a.team;
-    const int64_t share = (total + teams - 1) / teams;
-    const int64_t begin = team * share, end = min(total, begin + share);
+    const int teams = DEC_GRID / a.team;
+    run.team = wg / a.team, run.member = wg - run.team * a.team;
+    run.share = (total + teams - 1) / teams;
+    run.begin = run.team * run.share, run.end = min(total, run.begin + run.share);
     if (tid == 0) a.rec[wg] = make_int4(-1, 0, 0, 0);
-    if (begin >= end || team >= teams) return;
+    if (run.begin >= run.end || run.team >= teams) return false;
     int64_t before = 0;
-    for (int base = 0; base < a.N; base += DEC_THREADS) {
-        const int n = base + tid;
-        const int64_t own = base == 0 ? first : tiles_of(n);
+    for (int base = 0; base < a.N; base += THREADS) {
+        const int64_t own = base == 0 ? first : tiles_of(base + tid);
         int64_t sum = own;
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
@@ -158,17 +149,95 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
             if (i < w) lo += scan[i];
             chunk += scan[i];
         }
-        if (begin >= lo && begin < lo + own) {
-            found[0] = n;
+        if (run.begin >= lo && run.begin < lo + own) {
+            found[0] = base + tid;
             found[1] = lo;
         }
         before += chunk;
         __syncthreads();
-        if (before > begin) break;
+        if (before > run.begin) break;
     }
-    int n = __builtin_amdgcn_readfirstlane((int)found[0]);
-    int64_t unit0 = found[1];   // tile number at which sequence n begins
-    int64_t pos = begin;
+    run.n = __builtin_amdgcn_readfirstlane((int)found[0]);
+    run.unit0 = found[1];
+    return true;
+}
+
+// The next unit of a run at tile `pos`: false where there is none for this workgroup there, with pos
+// and the sequence moved on.
+struct Unit {
+    SeqInfo s;
+    int tiles, t0, t1, rb;
+    int64_t rows;
+};
+
+template <int M>
+__device__ __forceinline__ bool dec_unit(const LatentDecodeArgs& a, Run& run, int64_t& pos, Unit& u) {
+    u.s = dec_seq(a, run.n);
+    u.tiles = dec_tiles(u.s);
+    const int64_t all = (int64_t)dec_units<M>(a, u.s) * u.tiles;
+    if (pos >= run.unit0 + all) {
+        run.unit0 += all;
+        ++run.n;
+        return false;
+    }
+    const int unit = (int)((pos - run.unit0) / u.tiles);
+    u.t0 = (int)((pos - run.unit0) - (int64_t)unit * u.tiles);
+    u.t1 = (int)min((int64_t)u.tiles, u.t0 + (run.end - pos));
+    u.rb = unit * a.team + run.member;
+    u.rows = (int64_t)u.s.tokens * a.H;
+    if (u.rb >= dec_blocks<M>(a, u.s)) {   // the last team of a sequence may be short
+        pos += u.t1 - u.t0;
+        return false;
+    }
+    return true;
+}
+
+// This wave's share of a tile to LDS (kc, kr: offsets of the buffer; zeros: its start, for rows that are
+// not there).  row: this lane's cache row, of key `lane` of the tile.
+template <int NW>
+__device__ __forceinline__ void dec_load(const LatentDecodeArgs& a, uint32_t kc, uint32_t kr, char* zeros, int row, int w,
+                                         int lane) {
+    constexpr int KPW = DEC_KEYS / NW;   // keys that a wave copies
+    const int lane16 = fresh(lane * 16);
+#pragma unroll
+    for (int i = 0; i < KPW; ++i) {
+        const int key = KPW * w + i;
+        const int from = __builtin_amdgcn_readlane(row, key);
+        if (from >= 0) {
+            dma16(a.cache + (size_t)from * LROW, lane16 ^ ((key & 15) * 16), kc + key * (LC * 2));
+        } else {
+            *reinterpret_cast<uint4*>(zeros + key * (LC * 2) + lane16) = make_uint4(0, 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < KPW / 8; ++i) {
+        const int key = KPW * w + 8 * i + (lane >> 3);
+        const int at = max(__shfl(row, key, 64), 0);   // scores of absent keys are replaced
+        dma16(a.cache + (size_t)at * LROW + LC + (((lane & 7) ^ ((key >> 1) & 7)) * 8), kr + (KPW * w + 8 * i) * (LR * 2));
+    }
+}
+
+// workgroups go round the 8 XCDs: numbered so that neighbours, which read the same sequence, share an L2
+__device__ __forceinline__ int dec_wg() { return (blockIdx.x & 7) * (DEC_GRID / 8) + (blockIdx.x >> 3); }
+
+template <int MT, int NW, int KG>
+__global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeArgs a) {
+    constexpr int M = 16 * MT;
+    constexpr int KT = 4 / KG;                 // scores: key groups KG, 16-key tiles of a wave,
+    constexpr int RH = NW / KG, MQ = MT / RH;  // row parts, row tiles of a wave
+    constexpr int CT = 32 / NW;                // 16-column tiles of a wave in the values' product
+    __shared__ __align__(256) char kc[2][DEC_KEYS * LC * 2];
+    __shared__ __align__(256) char kr[2][DEC_KEYS * LR * 2];
+    __shared__ __align__(16) char pf[MT * 2 * 1024];   // P^T in operand order
+    __shared__ float mx[KG][M];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, q = lane >> 4;
+    const int kg = w % KG, rh = w / KG;        // the wave's keys and row part in the scores
+    const int wg = dec_wg();
+    Run run;
+    if (!dec_run<M, 64 * NW>(a, wg, run)) return;
+    int64_t pos = run.begin;
 
     const uint32_t kc0 = lds_offset(kc), kr0 = lds_offset(kr);
     // where this lane reads in a tile: key 16 KT kg + r, pieces 4 k + q (the exclusive or leaves bits 4
@@ -183,23 +252,12 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
     for (int c = 0; c < CT; ++c)
         v_at[c] = (4 * q + (r >> 2)) * (LC * 2) + ((2 * (CT * w + c) + ((r >> 1) & 1)) ^ (4 * q + (r >> 2))) * 16 +
                   (r & 1) * 8;
-    while (pos < end) {
-        const SeqInfo s = dec_seq(a, n);
-        const int tiles = dec_tiles(s), units = dec_units<M>(a, s);
-        if (pos >= unit0 + (int64_t)units * tiles) {
-            unit0 += (int64_t)units * tiles;
-            ++n;
-            continue;
-        }
-        const int unit = (int)((pos - unit0) / tiles);
-        const int t0 = (int)((pos - unit0) - (int64_t)unit * tiles);
-        const int t1 = (int)min((int64_t)tiles, t0 + (end - pos));
-        const int rb = unit * a.team + member;
-        if (rb >= dec_blocks<M>(a, s)) {   // the last team of a sequence may be short
-            pos += t1 - t0;
-            continue;
-        }
-        const int64_t rows = (int64_t)s.tokens * a.H;
+    while (pos < run.end) {
+        Unit u;
+        if (!dec_unit<M>(a, run, pos, u)) continue;
+        const SeqInfo s = u.s;
+        const int n = run.n, t0 = u.t0, t1 = u.t1, tiles = u.tiles, rb = u.rb;
+        const int64_t rows = u.rows;
 
         // ---- q of this block's rows, and each row's key limit
         bf16x8 qf[MQ][18];
@@ -229,26 +287,7 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
         }
 
         auto load_tile = [&](int buf, int row) {
-            // row: this lane's cache row of key 64 j + lane
-            const int lane16 = fresh(lane * 16);
-#pragma unroll
-            for (int i = 0; i < KPW; ++i) {
-                const int key = KPW * w + i;
-                const int from = __builtin_amdgcn_readlane(row, key);
-                if (from >= 0) {
-                    dma16(a.cache + (size_t)from * LROW, lane16 ^ ((key & 15) * 16),
-                          kc0 + buf * (DEC_KEYS * LC * 2) + key * (LC * 2));
-                } else {
-                    *reinterpret_cast<uint4*>(&kc[buf][key * (LC * 2) + lane16]) = make_uint4(0, 0, 0, 0);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < KPW / 8; ++i) {
-                const int key = KPW * w + 8 * i + (lane >> 3);
-                const int at = max(__shfl(row, key, 64), 0);   // scores of absent keys are replaced below
-                dma16(a.cache + (size_t)at * LROW + LC + (((lane & 7) ^ ((key >> 1) & 7)) * 8),
-                      kr0 + buf * (DEC_KEYS * LR * 2) + (KPW * w + 8 * i) * (LR * 2));
-            }
+            dec_load<NW>(a, kc0 + buf * (DEC_KEYS * LC * 2), kr0 + buf * (DEC_KEYS * LR * 2), kc[buf], row, w, lane);
         };
 
         const int page0 = dec_page(a, n, s.len, 64 * t0 + lane);
@@ -430,54 +469,80 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
             }
         }
         if (t0 == 0 && t1 < tiles && tid == 0)
-            a.rec[wg] = make_int4(n, rb, (int)((pos + tiles - 1) / share) - team + 1, 0);
+            a.rec[wg] = make_int4(n, rb, (int)((pos + tiles - 1) / run.share) - run.team + 1, 0);
         pos += t1 - t0;
     }
 }
 
-// Joins the partial sums of a unit that was cut: workgroup (wg, row) takes one row of the unit that
-// began in workgroup wg's run, its eight waves every eighth part each.
+// Joins the partial sums of units that were cut.  Workgroup (wg, i) serves the unit that began in
+// workgroup wg's run.  A unit of many parts (one long sequence over the whole device) takes a workgroup
+// for each row, whose eight waves take every eighth part; one of few parts a wave for each row, and
+// every eighth workgroup for eight rows.  (A workgroup a row for two parts each took 26 us for 256 units of
+// 64 rows, a wave a row 13 us; a wave a row for 128 parts would take 40 us where the waves together take 5.)
 constexpr int JOIN_WAVES = 8;
+
+struct Joined {
+    float acc[8];   // columns 8 lane ..
+    float m, l;
+};
+
+__device__ __forceinline__ Joined join_parts(const LatentDecodeArgs& a, int wg, int row, int M, int parts, int first, int step,
+                                             int lane) {
+    Joined x;
+    x.m = -INFINITY, x.l = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x.acc[e] = 0.f;
+#pragma unroll 4
+    for (int k = first; k < parts; k += step) {
+        const size_t slot = k == 0 ? 2 * wg + 1 : 2 * (size_t)(wg + k * a.team);
+        const float2 pm = a.part_ml[slot * M + row];
+        const f32x4* p = reinterpret_cast<const f32x4*>(a.part + (slot * M + row) * LC) + 2 * lane;
+        const f32x4 u = p[0], v = p[1];
+        const float now = fmaxf(x.m, pm.x);
+        const float ref = now == -INFINITY ? 0.f : now;
+        const float fa = ex2(x.m - ref), fb = ex2(pm.x - ref);
+        x.m = now;
+        x.l = x.l * fa + pm.y * fb;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x.acc[e] = x.acc[e] * fa + u[e] * fb;
+            x.acc[4 + e] = x.acc[4 + e] * fa + v[e] * fb;
+        }
+    }
+    return x;
+}
+
 template <int MT>
 __global__ __launch_bounds__(64 * JOIN_WAVES) void latent_join_kernel(LatentDecodeArgs a) {
     constexpr int M = 16 * MT;
-    __shared__ float sums[JOIN_WAVES][LC];
-    __shared__ float ml[JOIN_WAVES][2];
     const int wg = blockIdx.x / M, i = blockIdx.x % M;
     const int4 rec = a.rec[wg];
-    if (rec.x < 0) return;
-    const SeqInfo s = dec_seq(a, rec.x);
-    const int64_t grow = (int64_t)rec.y * M + i;
-    if (grow >= (int64_t)s.tokens * a.H) return;
-    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int parts = rec.z;
-    float m = -INFINITY, l = 0.f;
-    float acc[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int k = w; k < parts; k += JOIN_WAVES) {
-        const size_t slot = k == 0 ? 2 * wg + 1 : 2 * (size_t)(wg + k * a.team);
-        const float2 pm = a.part_ml[slot * M + i];
-        const float4* p = reinterpret_cast<const float4*>(a.part + (slot * M + i) * LC) + 2 * lane;
-        const float4 x = p[0], y = p[1];
-        const float now = fmaxf(m, pm.x);
-        const float ref = now == -INFINITY ? 0.f : now;
-        const float fa = ex2(m - ref), fb = ex2(pm.x - ref);
-        m = now;
-        l = l * fa + pm.y * fb;
-        acc[0] = acc[0] * fa + x.x * fb;
-        acc[1] = acc[1] * fa + x.y * fb;
-        acc[2] = acc[2] * fa + x.z * fb;
-        acc[3] = acc[3] * fa + x.w * fb;
-        acc[4] = acc[4] * fa + y.x * fb;
-        acc[5] = acc[5] * fa + y.y * fb;
-        acc[6] = acc[6] * fa + y.z * fb;
-        acc[7] = acc[7] * fa + y.w * fb;
+    // (the working ones of a unit differ from unit to unit: workgroups go round the 8 XCDs)
+    if (rec.x < 0 || (parts <= JOIN_WAVES && i % JOIN_WAVES != wg % JOIN_WAVES)) return;
+    const SeqInfo s = dec_seq(a, rec.x);
+    const int64_t rows = (int64_t)s.tokens * a.H - (int64_t)rec.y * M;   // of this block
+    const size_t out0 = (size_t)s.bos * a.H + (size_t)rec.y * M;
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (parts <= JOIN_WAVES) {
+        const int row = i - i % JOIN_WAVES + w;
+        if (row >= rows) return;
+        const Joined x = join_parts(a, wg, row, M, parts, 0, 1, lane);
+        const float inv = x.l > 0.f ? 1.f / x.l : x.l;
+        uint4 v;
+        v.x = pack_bf2(x.acc[0] * inv, x.acc[1] * inv), v.y = pack_bf2(x.acc[2] * inv, x.acc[3] * inv);
+        v.z = pack_bf2(x.acc[4] * inv, x.acc[5] * inv), v.w = pack_bf2(x.acc[6] * inv, x.acc[7] * inv);
+        *reinterpret_cast<uint4*>(a.o + (out0 + row) * LC + 8 * lane) = v;
+        if (a.lse && lane == 0) a.lse[out0 + row] = x.l == 0.f ? -INFINITY : LN2 * (x.m + lg2(x.l));
+        return;
     }
+    if (i >= rows) return;
+    __shared__ float sums[JOIN_WAVES][LC];
+    __shared__ float ml[JOIN_WAVES][2];
+    const Joined x = join_parts(a, wg, i, M, parts, w, JOIN_WAVES, lane);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[w][8 * lane + e] = acc[e];
-    if (lane == 0) ml[w][0] = m, ml[w][1] = l;
+    for (int e = 0; e < 8; ++e) sums[w][8 * lane + e] = x.acc[e];
+    if (lane == 0) ml[w][0] = x.m, ml[w][1] = x.l;
     __syncthreads();
     float top = -INFINITY, sum = 0.f, v = 0.f;
 #pragma unroll
@@ -491,9 +556,8 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void latent_join_kernel(LatentDeco
         v += sums[k][c] * f;
     }
     const float inv = sum > 0.f ? 1.f / sum : sum;
-    const size_t out = (size_t)s.bos * a.H + grow;
-    a.o[out * LC + c] = f2bf(v * inv);
-    if (a.lse && c == 0) a.lse[out] = sum == 0.f ? -INFINITY : LN2 * (top + lg2(sum));
+    a.o[(out0 + i) * LC + c] = f2bf(v * inv);
+    if (a.lse && c == 0) a.lse[out0 + i] = sum == 0.f ? -INFINITY : LN2 * (top + lg2(sum));
 }
 
 // One wave a token: 64 16-byte pieces of the latent and 8 of the rope part into the cache row that
@@ -521,9 +585,11 @@ int dec_m(const cdr_latent_decode_problem* p) {
     return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-template <int MT, int NW, int KG>
+template <int MT>
 hipError_t launch_latent_decode(const LatentDecodeArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((latent_decode_kernel<MT, NW, KG>), dim3(DEC_GRID), dim3(64 * NW), 0, s, a);
+    if constexpr (MT == 1) hipLaunchKernelGGL((latent_decode_kernel<1, 4, 4>), dim3(DEC_GRID), dim3(256), 0, s, a);
+    else if constexpr (MT == 2) hipLaunchKernelGGL((latent_decode_kernel<2, 8, 4>), dim3(DEC_GRID), dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((latent_decode_kernel<4, 8, 2>), dim3(DEC_GRID), dim3(512), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((latent_join_kernel<MT>), dim3(DEC_GRID * 16 * MT), dim3(64 * JOIN_WAVES), 0, s, a);
@@ -595,9 +661,9 @@ cdr_status cdr_latent_decode_fwd(const cdr_latent_decode_problem* p, const void*
     const int64_t blocks = ((int64_t)p->T * p->H + m - 1) / m;
     a.team = p->varlen ? 1 : (int)(blocks < cdr::DEC_TEAM ? blocks : cdr::DEC_TEAM);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = m == 16   ? cdr::launch_latent_decode<1, 4, 4>(a, s)
-                         : m == 32 ? cdr::launch_latent_decode<2, 8, 4>(a, s)
-                                   : cdr::launch_latent_decode<4, 8, 2>(a, s);
+    const hipError_t e = m == 16   ? cdr::launch_latent_decode<1>(a, s)
+                         : m == 32 ? cdr::launch_latent_decode<2>(a, s)
+                                   : cdr::launch_latent_decode<4>(a, s);
     return e == hipSuccess ? CDR_OK : CDR_ERR_HIP;
 }
 

@@ -37,24 +37,6 @@ constexpr int AQ = AN + LR;   // a query's
 constexpr int A_ROWS = 128;   // rows (or keys) of a workgroup
 constexpr int A_TILE = 64;    // rows of a streamed tile
 
-typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
-
-__device__ __forceinline__ f32x16 mma(const bf16x8& a, const bf16x8& b, const f32x16& c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x16 zero16() {
-    f32x16 z;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = 0.f;
-    return z;
-}
-// registers 8 t .. 8 t + 7 of a result as the right operand of the next product
-__device__ __forceinline__ bf16x8 operand(const f32x16& p, int t) {
-    const uint4 v = make_uint4(pack_bf2(p[8 * t], p[8 * t + 1]), pack_bf2(p[8 * t + 2], p[8 * t + 3]),
-                               pack_bf2(p[8 * t + 4], p[8 * t + 5]), pack_bf2(p[8 * t + 6], p[8 * t + 7]));
-    return __builtin_bit_cast(bf16x8, v);
-}
-
 struct LatentAttnArgs {
     const uint16_t* q;
     const uint16_t* k;
@@ -73,10 +55,6 @@ struct LatentAttnArgs {
     int T, Tk, H, N, slots, total_k;
     float scale, scale2;
 };
-
-// offsets within a tile: row pitch 256 bytes (16 pieces) and 128 bytes (8 pieces)
-__device__ __forceinline__ int f16(int row) { return ((row & 7) << 1) | ((row >> 3) & 1); }
-__device__ __forceinline__ int f8(int row) { return (((row >> 1) & 3) << 1) | ((row >> 3) & 1); }
 
 struct Seq {
     int64_t q0, k0;    // first row and key
@@ -261,7 +239,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
                 sum += sc[t][i];
             }
         l = l * alpha + sum;
-        if (!__all(alpha == 1.f)) {
+        if (__builtin_expect(!__all(alpha == 1.f), 0)) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
