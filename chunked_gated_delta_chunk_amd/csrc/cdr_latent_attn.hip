@@ -36,6 +36,7 @@ constexpr int AV = 128;       // value dimensions
 constexpr int AQ = AN + LR;   // a query's
 constexpr int A_ROWS = 128;   // rows (or keys) of a workgroup
 constexpr int A_TILE = 64;    // rows of a streamed tile
+constexpr int A_LDS = 2 * A_TILE * (256 + 128 + 256);   // two tiles of 320 dimensions
 
 struct LatentAttnArgs {
     const uint16_t* q;
@@ -45,7 +46,7 @@ struct LatentAttnArgs {
     const int32_t* cuq;
     const int32_t* cuk;
     const uint16_t* d_o;
-    const float* delta;
+    float* delta;
     uint16_t* o;        // forward: o; dq kernel: dq
     float* lse;
     uint16_t* dk;
@@ -163,7 +164,7 @@ __device__ __forceinline__ void load_keys(const LatentAttnArgs& a, const Seq& s,
 }
 
 __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
-    __shared__ __align__(256) char lds[2 * A_TILE * (256 + 128 + 256)];
+    __shared__ __align__(256) char lds[A_LDS];
     char* kn = lds;
     char* kr = kn + 2 * A_TILE * 256;
     char* vt = kr + 2 * A_TILE * 128;
@@ -204,14 +205,27 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
         const char* tn = kn + buf * A_TILE * 256;
         const char* tr = kr + buf * A_TILE * 128;
         const char* tv = vt + buf * A_TILE * 256;
-        f32x16 sc[2];
+        f32x16 sc[2] = {zero16(), zero16()};
+        bf16x8 f[2][2][2];
+        auto read_keys = [&](int batch) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            sc[t] = zero16();
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sc[t] = mma(row256(tn, t, k, lane), qf[k], sc[t]);
+                for (int t = 0; t < 2; ++t) {
+                    const int k = 2 * batch + i;
+                    f[batch & 1][i][t] = k < 8 ? row256(tn, t, k, lane) : row128(tr, t, k - 8, lane);
+                }
+        };
+        read_keys(0);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sc[t] = mma(row128(tr, t, k, lane), qf[8 + k], sc[t]);
+        for (int batch = 0; batch < 6; ++batch) {
+            if (batch < 5) read_keys(batch + 1);
+            keep_order();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) sc[t] = mma(f[batch & 1][i][t], qf[2 * batch + i], sc[t]);
+            keep_order();
         }
         if ((j + 1) * A_TILE > lim_first) {
 #pragma unroll
@@ -265,32 +279,14 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     if (lane < 32) a.lse[out] = l == 0.f ? -INFINITY : LN2 * (m + lg2(l));
 }
 
-// delta = do . o of every row and head: 16 lanes a row
-__global__ __launch_bounds__(256) void latent_delta_kernel(const uint16_t* o, const uint16_t* d_o, float* delta, int64_t rows) {
-    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    const int i = threadIdx.x & 15;
-    float x[8], y[8], t = 0.f;
-    if (row < rows) {
-        unpack8(*reinterpret_cast<const uint4*>(o + row * AV + 8 * i), x);
-        unpack8(*reinterpret_cast<const uint4*>(d_o + row * AV + 8 * i), y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t += x[e] * y[e];
-    }
-#pragma unroll
-    for (int k = 1; k < 16; k <<= 1) t += __shfl_xor(t, k, 64);
-    if (row < rows && i == 0) delta[row] = t;
-}
-
-__global__ __launch_bounds__(256, 2) void latent_dq_kernel(LatentAttnArgs a) {
-    __shared__ __align__(256) char lds[2 * A_TILE * (256 + 128 + 256)];
+// dq of a block of 128 rows, or with DELTA its delta as sum_j p_ij (do_i . v_j): nothing of the loop but the scores
+// and dp then.
+template <bool DELTA>
+__device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, const Seq& s, int h, int block) {
     char* kn = lds;
     char* kr = kn + 2 * A_TILE * 256;
     char* vt = kr + 2 * A_TILE * 128;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int h = blockIdx.x % a.H;
-    int n, block;
-    if (!attn_slot(a, a.cuq, a.T, a.slots - 1 - blockIdx.x / a.H, n, block)) return;
-    const Seq s = attn_seq(a, n);
     const Tiles at = {lds_offset(kn), lds_offset(kr), lds_offset(vt)};
     const int row = block * A_ROWS + 32 * w + (lane & 31);
     const int use = min(row, s.lq - 1);
@@ -312,10 +308,11 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(LatentAttnArgs a) {
     }
     float lse = a.lse[in] * LOG2E;
     if (lse == -INFINITY) lse = INFINITY;   // a row without keys: all its weights are zero
-    const float delta = a.delta[in];
-    f32x16 dq[6];
+    float delta = DELTA ? 0.f : a.delta[in];
+    f32x16 dq[DELTA ? 1 : 6];
+    if constexpr (!DELTA)
 #pragma unroll
-    for (int c = 0; c < 6; ++c) dq[c] = zero16();
+        for (int c = 0; c < 6; ++c) dq[c] = zero16();
 
     if (tiles > 0) load_keys(a, s, h, 0, 0, at, w, lane);
     for (int j = 0; j < tiles; ++j) {
@@ -341,8 +338,10 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(LatentAttnArgs a) {
             for (int i = 0; i < 16; ++i) {
                 float p = ex2(sc[i] * a.scale2 - lse);
                 if (cut && j * A_TILE + 32 * t + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= lim) p = 0.f;
-                dp[i] = p * (dp[i] - delta);
+                if constexpr (DELTA) delta += p * dp[i];
+                else dp[i] = p * (dp[i] - delta);
             }
+            if constexpr (!DELTA)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const bf16x8 d = operand(dp, u);
@@ -353,16 +352,60 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(LatentAttnArgs a) {
             }
         }
     }
-    if (row >= s.lq) return;
     const size_t out = (size_t)(s.q0 + row) * a.H + h;
+    if constexpr (DELTA) {
+        delta += __shfl_xor(delta, 32, 64);
+        if (row < s.lq && lane < 32) a.delta[out] = delta;
+        return;
+    }
+    if (row >= s.lq) return;
 #pragma unroll
     for (int c = 0; c < 6; ++c)
 #pragma unroll
         for (int g = 0; g < 4; ++g) put4(a.o + out * AQ + 32 * c + 8 * g + 4 * (lane >> 5), dq[c], g, a.scale);
 }
 
+__global__ __launch_bounds__(256, 2) void latent_dq_kernel(LatentAttnArgs a) {
+    __shared__ __align__(256) char lds[A_LDS];
+    const int h = blockIdx.x % a.H;
+    int n, block;
+    if (!attn_slot(a, a.cuq, a.T, a.slots - 1 - blockIdx.x / a.H, n, block)) return;
+    dq_block<false>(a, lds, attn_seq(a, n), h, block);
+}
+
+// delta of a block of 128 rows: do . o from the forward's o, 16 lanes a row; but where the rows see at most 128
+// keys, from the weights themselves.  There ds is a difference of two numbers of one size (a row of one key
+// has ds = 0), o is large and its rounding to bf16 would be a tenth of the error of dq and dk; behind many keys
+// o is an average and its rounding counts little.
+__global__ __launch_bounds__(256, 2) void latent_delta_kernel(LatentAttnArgs a, const uint16_t* o) {
+    __shared__ __align__(256) char lds[A_LDS];
+    const int h = blockIdx.x % a.H;
+    int n, block;
+    if (!attn_slot(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;
+    const Seq s = attn_seq(a, n);
+    const int last = min(block * A_ROWS + A_ROWS, s.lq) - 1;
+    if (s.lk - s.lq + last + 1 <= 2 * A_TILE) {
+        dq_block<true>(a, lds, s, h, block);
+        return;
+    }
+    const int i = threadIdx.x & 15;
+#pragma unroll 4
+    for (int r = 0; r < A_ROWS / 16; ++r) {
+        const int row = block * A_ROWS + 16 * r + (threadIdx.x >> 4);
+        const size_t at = (size_t)(s.q0 + min(row, last)) * a.H + h;
+        float x[8], y[8], t = 0.f;
+        unpack8(*reinterpret_cast<const uint4*>(o + at * AV + 8 * i), x);
+        unpack8(*reinterpret_cast<const uint4*>(a.d_o + at * AV + 8 * i), y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t += x[e] * y[e];
+#pragma unroll
+        for (int k = 1; k < 16; k <<= 1) t += __shfl_xor(t, k, 64);
+        if (row <= last && i == 0) a.delta[at] = t;
+    }
+}
+
 __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
-    __shared__ __align__(256) char lds[2 * A_TILE * (256 + 128 + 256)];
+    __shared__ __align__(256) char lds[A_LDS];
     __shared__ __align__(16) float stat[2][2][A_TILE];   // lse (base 2) and delta of a tile's rows
     char* qn = lds;
     char* qr = qn + 2 * A_TILE * 256;
@@ -586,8 +629,7 @@ cdr_status cdr_latent_attn_bwd(const cdr_latent_attn_problem* p, const void* q, 
     if (need > 0 && (!workspace || !cdr::aligned16(workspace) || workspace_bytes < need)) return CDR_ERR_WORKSPACE;
     hipStream_t s = static_cast<hipStream_t>(stream);
     cdr::LatentAttnArgs a = cdr::attn_args(p, q, k_nope, k_rope, v, cu_seqlens, cu_seqlens_k);
-    float* delta = static_cast<float*>(workspace);
-    a.delta = delta;
+    a.delta = static_cast<float*>(workspace);
     a.dkr = reinterpret_cast<float*>(static_cast<char*>(workspace) + cdr::up16((size_t)tq * p->H * sizeof(float)));
     a.lse = const_cast<float*>(lse);
     a.d_o = static_cast<const uint16_t*>(d_o);
@@ -595,11 +637,10 @@ cdr_status cdr_latent_attn_bwd(const cdr_latent_attn_problem* p, const void* q, 
     a.dk = static_cast<uint16_t*>(dk_nope);
     a.dv = static_cast<uint16_t*>(dv);
     if (tq > 0) {
-        const int64_t rows = tq * p->H;
-        hipLaunchKernelGGL(cdr::latent_delta_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, s,
-                           static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(d_o), delta, rows);
-        if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
         a.slots = (int)cdr::attn_slots(p->T, p);
+        hipLaunchKernelGGL(cdr::latent_delta_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a,
+                           static_cast<const uint16_t*>(o));
+        if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
         hipLaunchKernelGGL(cdr::latent_dq_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a);
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
     }
