@@ -35,6 +35,7 @@ constexpr int AN = 128;       // nope dimensions
 constexpr int AV = 128;       // value dimensions
 constexpr int AQ = AN + LR;   // a query's
 constexpr int A_ROWS = 128;   // rows (or keys) of a workgroup
+constexpr int DQ_ROWS = 256;  // rows of a workgroup of the dq kernel
 constexpr int A_TILE = 64;    // rows of a streamed tile
 constexpr int A_LDS = 2 * A_TILE * (256 + 128 + 256);   // two tiles of 320 dimensions
 
@@ -77,10 +78,11 @@ __device__ __forceinline__ Seq attn_seq(const LatentAttnArgs& a, int n) {
 }
 
 // Sequence and block of a slot: as in the chunk map, sequence n owns the slots from
-// cu[n] / A_ROWS + n on (packed), or n * ceil(T / A_ROWS) on.  False for an unused slot.
+// cu[n] / ROWS + n on (packed), or n * ceil(T / ROWS) on.  False for an unused slot.
+template <int ROWS>
 __device__ __forceinline__ bool attn_slot(const LatentAttnArgs& a, const int32_t* cu, int T, int slot, int& n, int& block) {
     if (cu == nullptr) {
-        const int per = (T + A_ROWS - 1) / A_ROWS;
+        const int per = (T + ROWS - 1) / ROWS;
         n = slot / per;
         block = slot - n * per;
         return true;
@@ -88,62 +90,82 @@ __device__ __forceinline__ bool attn_slot(const LatentAttnArgs& a, const int32_t
     int lo = 0, hi = a.N - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (min(max(cu[mid], 0), T) / A_ROWS + mid <= slot) lo = mid; else hi = mid - 1;
+        if (min(max(cu[mid], 0), T) / ROWS + mid <= slot) lo = mid; else hi = mid - 1;
     }
     n = lo;
     const int b = min(max(cu[n], 0), T);
-    block = slot - (b / A_ROWS + n);
-    return block >= 0 && block * A_ROWS < min(max(cu[n + 1], b), T) - b;
+    block = slot - (b / ROWS + n);
+    return block >= 0 && block * ROWS < min(max(cu[n + 1], b), T) - b;
 }
 
 // Copies rows `first` .. + 63 (clipped to `last`) of an array with 256-byte or 128-byte rows to LDS:
-// this wave's quarter.  base: row 0; stride: bytes between rows.
+// this wave's share of NW.  base: row 0; stride: bytes between rows.
+template <int NW>
 __device__ __forceinline__ void copy256(const void* base, int64_t first, int64_t last, uint32_t stride, uint32_t lds, int w,
                                         int lane) {
     const char* b = static_cast<const char*>(base) + first * stride;
     const int top = (int)min(last - first, (int64_t)63);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = 4 * (w + 4 * i) + (lane >> 4);
+    for (int i = 0; i < 16 / NW; ++i) {
+        const int row = 4 * (w + NW * i) + (lane >> 4);
         const uint32_t off = __umul24(min(row, top), stride) + (((lane & 15) ^ f16(row)) * 16);
-        dma16(b, off, lds + 1024 * (w + 4 * i));
+        dma16(b, off, lds + 1024 * (w + NW * i));
     }
 }
+template <int NW>
 __device__ __forceinline__ void copy128(const void* base, int64_t first, int64_t last, uint32_t stride, uint32_t lds, int w,
                                         int lane) {
     const char* b = static_cast<const char*>(base) + first * stride;
     const int top = (int)min(last - first, (int64_t)63);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = 8 * (w + 4 * i) + (lane >> 3);
+    for (int i = 0; i < 8 / NW; ++i) {
+        const int row = 8 * (w + NW * i) + (lane >> 3);
         const uint32_t off = __umul24(min(row, top), stride) + (((lane & 7) ^ f8(row)) * 16);
-        dma16(b, off, lds + 1024 * (w + 4 * i));
+        dma16(b, off, lds + 1024 * (w + NW * i));
     }
 }
 
-// left operand of 16 contracted dimensions (step s): rows 32 t + (lane & 31) of a tile
-__device__ __forceinline__ bf16x8 row256(const char* tile, int t, int s, int lane) {
-    const int r = lane & 31;
-    return lds16(tile + t * 32 * 256 + r * 256 + (((2 * s + (lane >> 5)) ^ f16(r)) * 16));
-}
-__device__ __forceinline__ bf16x8 row128(const char* tile, int t, int s, int lane) {
-    const int r = lane & 31;
-    return lds16(tile + t * 32 * 128 + r * 128 + (((2 * s + (lane >> 5)) ^ f8(r)) * 16));
-}
-// left operand of 16 contracted rows (step s: rows 16 s ..) for columns 32 c + (lane & 31) of a tile, the
-// rows in the order 8 (i / 4) + 4 (lane / 32) + i % 4 of a result's registers
-__device__ __forceinline__ bf16x8 col256(const char* tile, int s, int c, int lane) {
-    const int i = lane & 15, row = 4 * (lane >> 5) + (i >> 2);
-    const int piece = 4 * c + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
-    const char* p = tile + (16 * s + row) * 256 + (i & 1) * 8;
-    return join8(lds_tr(p + ((piece ^ f16(row)) * 16)), lds_tr(p + 8 * 256 + ((piece ^ f16(row + 8)) * 16)));
-}
-__device__ __forceinline__ bf16x8 col128(const char* tile, int s, int c, int lane) {
-    const int i = lane & 15, row = 4 * (lane >> 5) + (i >> 2);
-    const int piece = 4 * c + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
-    const char* p = tile + (16 * s + row) * 128 + (i & 1) * 8;
-    return join8(lds_tr(p + ((piece ^ f8(row)) * 16)), lds_tr(p + 8 * 128 + ((piece ^ f8(row + 8)) * 16)));
-}
+// Where a lane reads in a tile.  The exclusive or with f16 or f8 leaves a step's or column tile's part of the
+// offset free, so each read is a base, one exclusive or with a constant and a fixed step; `again` keeps
+// the compiler from holding every one of them in a register over the loop.
+struct Reads {
+    int r256, r128, c256[2], c128[2];
+    __device__ __forceinline__ explicit Reads(int lane) {
+        const int r = lane & 31, i = lane & 15, piece = 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
+        r256 = r * 256 + (((lane >> 5) ^ f16(r)) * 16);
+        r128 = r * 128 + (((lane >> 5) ^ f8(r)) * 16);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int row = 8 * g + 4 * (lane >> 5) + (i >> 2);
+            c256[g] = row * 256 + ((piece ^ f16(row)) * 16) + (i & 1) * 8;
+            c128[g] = row * 128 + ((piece ^ f8(row)) * 16) + (i & 1) * 8;
+        }
+    }
+    __device__ __forceinline__ Reads again() const {
+        Reads x = *this;
+        x.r256 = fresh(r256), x.r128 = fresh(r128);
+        x.c256[0] = fresh(c256[0]), x.c256[1] = fresh(c256[1]);
+        x.c128[0] = fresh(c128[0]), x.c128[1] = fresh(c128[1]);
+        return x;
+    }
+    // left operand of 16 contracted dimensions (step s): rows 32 t + (lane & 31) of a tile
+    __device__ __forceinline__ bf16x8 row256(const char* tile, int t, int s) const {
+        return lds16(tile + t * 32 * 256 + (r256 ^ (32 * s)));
+    }
+    __device__ __forceinline__ bf16x8 row128(const char* tile, int t, int s) const {
+        return lds16(tile + t * 32 * 128 + (r128 ^ (32 * s)));
+    }
+    // left operand of 16 contracted rows (step s: rows 16 s ..) for columns 32 c + (lane & 31) of a tile, the
+    // rows in the order 8 (i / 4) + 4 (lane / 32) + i % 4 of a result's registers
+    __device__ __forceinline__ bf16x8 col256(const char* tile, int s, int c) const {
+        const char* p = tile + s * 16 * 256;
+        return join8(lds_tr(p + (c256[0] ^ (64 * c))), lds_tr(p + (c256[1] ^ (64 * c))));
+    }
+    __device__ __forceinline__ bf16x8 col128(const char* tile, int s, int c) const {
+        const char* p = tile + s * 16 * 128;
+        return join8(lds_tr(p + (c128[0] ^ (64 * c))), lds_tr(p + (c128[1] ^ (64 * c))));
+    }
+};
 
 // four neighbouring columns of a transposed result as bf16
 __device__ __forceinline__ void put4(uint16_t* p, const f32x16& x, int g, float f) {
@@ -155,12 +177,13 @@ struct Tiles {
     uint32_t kn, kr, v;   // LDS offsets of buffer 0
 };
 
+template <int NW>
 __device__ __forceinline__ void load_keys(const LatentAttnArgs& a, const Seq& s, int h, int tile, int buf, const Tiles& at,
                                           int w, int lane) {
     const int64_t first = (int64_t)tile * A_TILE, last = s.lk - 1;
-    copy256(a.k + s.k0 * a.kt + h * a.kh, first, last, (uint32_t)a.kt * 2, at.kn + buf * A_TILE * 256, w, lane);
-    copy128(a.kr + s.k0 * a.rt, first, last, (uint32_t)a.rt * 2, at.kr + buf * A_TILE * 128, w, lane);
-    copy256(a.v + s.k0 * a.vt + h * a.vh, first, last, (uint32_t)a.vt * 2, at.v + buf * A_TILE * 256, w, lane);
+    copy256<NW>(a.k + s.k0 * a.kt + h * a.kh, first, last, (uint32_t)a.kt * 2, at.kn + buf * A_TILE * 256, w, lane);
+    copy128<NW>(a.kr + s.k0 * a.rt, first, last, (uint32_t)a.rt * 2, at.kr + buf * A_TILE * 128, w, lane);
+    copy256<NW>(a.v + s.k0 * a.vt + h * a.vh, first, last, (uint32_t)a.vt * 2, at.v + buf * A_TILE * 256, w, lane);
 }
 
 __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
@@ -171,9 +194,10 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = blockIdx.x % a.H;
     int n, block;
-    if (!attn_slot(a, a.cuq, a.T, a.slots - 1 - blockIdx.x / a.H, n, block)) return;
+    if (!attn_slot<A_ROWS>(a, a.cuq, a.T, a.slots - 1 - blockIdx.x / a.H, n, block)) return;
     const Seq s = attn_seq(a, n);
     const Tiles at = {lds_offset(kn), lds_offset(kr), lds_offset(vt)};
+    const Reads reads(lane);
 
     // this lane's row, and the keys it sees
     const int row = block * A_ROWS + 32 * w + (lane & 31);
@@ -195,13 +219,14 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     for (int c = 0; c < 4; ++c) o[c] = zero16();
     float m = -INFINITY, l = 0.f;
 
-    if (tiles > 0) load_keys(a, s, h, 0, 0, at, w, lane);
+    if (tiles > 0) load_keys<4>(a, s, h, 0, 0, at, w, lane);
     for (int j = 0; j < tiles; ++j) {
         const int buf = j & 1;
         dma_wait();
         __syncthreads();
-        if (j + 1 < tiles) load_keys(a, s, h, j + 1, buf ^ 1, at, w, lane);
+        if (j + 1 < tiles) load_keys<4>(a, s, h, j + 1, buf ^ 1, at, w, lane);
         if (j * A_TILE >= lim_last) continue;   // all of this wave's rows end before this tile
+        const Reads x = reads.again();
         const char* tn = kn + buf * A_TILE * 256;
         const char* tr = kr + buf * A_TILE * 128;
         const char* tv = vt + buf * A_TILE * 256;
@@ -213,7 +238,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const int k = 2 * batch + i;
-                    f[batch & 1][i][t] = k < 8 ? row256(tn, t, k, lane) : row128(tr, t, k - 8, lane);
+                    f[batch & 1][i][t] = k < 8 ? x.row256(tn, t, k) : x.row128(tr, t, k - 8);
                 }
         };
         read_keys(0);
@@ -265,7 +290,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
             for (int u = 0; u < 2; ++u) {
                 const bf16x8 p = operand(sc[t], u);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) o[c] = mma(col256(tv, 2 * t + u, c, lane), p, o[c]);
+                for (int c = 0; c < 4; ++c) o[c] = mma(x.col256(tv, 2 * t + u, c), p, o[c]);
             }
     }
     l += __shfl_xor(l, 32, 64);
@@ -279,32 +304,44 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     if (lane < 32) a.lse[out] = l == 0.f ? -INFINITY : LN2 * (m + lg2(l));
 }
 
-// dq of a block of 128 rows, or with DELTA its delta as sum_j p_ij (do_i . v_j): nothing of the loop but the scores
-// and dp then.
-template <bool DELTA>
+// dq of a block of 32 NW rows, or with DELTA its delta as sum_j p_ij (do_i . v_j): nothing of the loop but the
+// scores and dp then.  For dq a wave holds 48 registers of q and 96 of sums; do, 32 more, stays in LDS (`mine`),
+// without which the loop spilled and each spill's reload waited for the copies under way.
+template <bool DELTA, int NW>
 __device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, const Seq& s, int h, int block) {
+    constexpr int ROWS = 32 * NW;
     char* kn = lds;
     char* kr = kn + 2 * A_TILE * 256;
     char* vt = kr + 2 * A_TILE * 128;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Tiles at = {lds_offset(kn), lds_offset(kr), lds_offset(vt)};
-    const int row = block * A_ROWS + 32 * w + (lane & 31);
+    const Reads reads(lane);
+    const int row = block * ROWS + 32 * w + (lane & 31);
     const int use = min(row, s.lq - 1);
     const int lim = min(s.lk, s.lk - s.lq + use + 1);
-    const int lim_first = min(s.lk, s.lk - s.lq + min(block * A_ROWS + 32 * w, s.lq - 1) + 1);
-    const int lim_last = min(s.lk, s.lk - s.lq + min(block * A_ROWS + 32 * w + 31, s.lq - 1) + 1);
-    const int keys = min(s.lk, s.lk - s.lq + min(block * A_ROWS + A_ROWS - 1, s.lq - 1) + 1);
+    const int lim_first = min(s.lk, s.lk - s.lq + min(block * ROWS + 32 * w, s.lq - 1) + 1);
+    const int lim_last = min(s.lk, s.lk - s.lq + min(block * ROWS + 32 * w + 31, s.lq - 1) + 1);
+    const int keys = min(s.lk, s.lk - s.lq + min(block * ROWS + ROWS - 1, s.lq - 1) + 1);
     const int tiles = keys > 0 ? (keys + A_TILE - 1) / A_TILE : 0;
 
     const size_t in = (size_t)(s.q0 + use) * a.H + h;
-    bf16x8 qf[12], df[8];
+    bf16x8 qf[12], df[DELTA ? 8 : 1];
+    char* mine = lds + A_LDS + w * 32 * 256;
     {
         const uint16_t* q = a.q + (s.q0 + use) * a.qt + h * a.qh + 8 * (lane >> 5);
 #pragma unroll
         for (int k = 0; k < 12; ++k) qf[k] = *reinterpret_cast<const bf16x8*>(q + 16 * k);
-        const uint16_t* d = a.d_o + in * AV + 8 * (lane >> 5);
+        if constexpr (DELTA) {
+            const uint16_t* d = a.d_o + in * AV + 8 * (lane >> 5);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) df[k] = *reinterpret_cast<const bf16x8*>(d + 16 * k);
+            for (int k = 0; k < 8; ++k) df[k] = *reinterpret_cast<const bf16x8*>(d + 16 * k);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = 4 * i + (lane >> 4), at_row = min(block * ROWS + 32 * w + r, s.lq - 1);
+                dma16(a.d_o + ((size_t)(s.q0 + at_row) * a.H + h) * AV + ((lane & 15) ^ f16(r)) * 8, lds_offset(mine) + 1024 * i);
+            }
+        }
     }
     float lse = a.lse[in] * LOG2E;
     if (lse == -INFINITY) lse = INFINITY;   // a row without keys: all its weights are zero
@@ -314,25 +351,27 @@ __device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, con
 #pragma unroll
         for (int c = 0; c < 6; ++c) dq[c] = zero16();
 
-    if (tiles > 0) load_keys(a, s, h, 0, 0, at, w, lane);
+    if (tiles > 0) load_keys<NW>(a, s, h, 0, 0, at, w, lane);
     for (int j = 0; j < tiles; ++j) {
         const int buf = j & 1;
         dma_wait();
         __syncthreads();
-        if (j + 1 < tiles) load_keys(a, s, h, j + 1, buf ^ 1, at, w, lane);
+        if (j + 1 < tiles) load_keys<NW>(a, s, h, j + 1, buf ^ 1, at, w, lane);
+        const Reads x = reads.again();
         const char* tn = kn + buf * A_TILE * 256;
         const char* tr = kr + buf * A_TILE * 128;
         const char* tv = vt + buf * A_TILE * 256;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             if (j * A_TILE + 32 * t >= lim_last) break;
+            const Reads again = reads.again();   // do's own reads: not kept from one half to the next
             f32x16 sc = zero16(), dp = zero16();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sc = mma(row256(tn, t, k, lane), qf[k], sc);
+            for (int k = 0; k < 8; ++k) sc = mma(x.row256(tn, t, k), qf[k], sc);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sc = mma(row128(tr, t, k, lane), qf[8 + k], sc);
+            for (int k = 0; k < 4; ++k) sc = mma(x.row128(tr, t, k), qf[8 + k], sc);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dp = mma(row256(tv, t, k, lane), df[k], dp);
+            for (int k = 0; k < 8; ++k) dp = mma(x.row256(tv, t, k), DELTA ? df[DELTA ? k : 0] : again.row256(mine, 0, k), dp);
             const bool cut = j * A_TILE + 32 * t + 32 > lim_first;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -346,9 +385,9 @@ __device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, con
             for (int u = 0; u < 2; ++u) {
                 const bf16x8 d = operand(dp, u);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) dq[c] = mma(col256(tn, 2 * t + u, c, lane), d, dq[c]);
+                for (int c = 0; c < 4; ++c) dq[c] = mma(x.col256(tn, 2 * t + u, c), d, dq[c]);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) dq[4 + c] = mma(col128(tr, 2 * t + u, c, lane), d, dq[4 + c]);
+                for (int c = 0; c < 2; ++c) dq[4 + c] = mma(x.col128(tr, 2 * t + u, c), d, dq[4 + c]);
             }
         }
     }
@@ -365,12 +404,12 @@ __device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, con
         for (int g = 0; g < 4; ++g) put4(a.o + out * AQ + 32 * c + 8 * g + 4 * (lane >> 5), dq[c], g, a.scale);
 }
 
-__global__ __launch_bounds__(256, 2) void latent_dq_kernel(LatentAttnArgs a) {
-    __shared__ __align__(256) char lds[A_LDS];
+__global__ __launch_bounds__(2 * DQ_ROWS, 2) void latent_dq_kernel(LatentAttnArgs a) {
+    __shared__ __align__(256) char lds[A_LDS + DQ_ROWS * 256];
     const int h = blockIdx.x % a.H;
     int n, block;
-    if (!attn_slot(a, a.cuq, a.T, a.slots - 1 - blockIdx.x / a.H, n, block)) return;
-    dq_block<false>(a, lds, attn_seq(a, n), h, block);
+    if (!attn_slot<DQ_ROWS>(a, a.cuq, a.T, a.slots - 1 - blockIdx.x / a.H, n, block)) return;
+    dq_block<false, DQ_ROWS / 32>(a, lds, attn_seq(a, n), h, block);
 }
 
 // delta of a block of 128 rows: do . o from the forward's o, 16 lanes a row; but where the rows see at most 128
@@ -381,11 +420,11 @@ __global__ __launch_bounds__(256, 2) void latent_delta_kernel(LatentAttnArgs a, 
     __shared__ __align__(256) char lds[A_LDS];
     const int h = blockIdx.x % a.H;
     int n, block;
-    if (!attn_slot(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;
+    if (!attn_slot<A_ROWS>(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;
     const Seq s = attn_seq(a, n);
     const int last = min(block * A_ROWS + A_ROWS, s.lq) - 1;
     if (s.lk - s.lq + last + 1 <= 2 * A_TILE) {
-        dq_block<true>(a, lds, s, h, block);
+        dq_block<true, A_ROWS / 32>(a, lds, s, h, block);
         return;
     }
     const int i = threadIdx.x & 15;
@@ -414,8 +453,9 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = blockIdx.x % a.H;
     int n, block;
-    if (!attn_slot(a, a.cuk, a.Tk, blockIdx.x / a.H, n, block)) return;
+    if (!attn_slot<A_ROWS>(a, a.cuk, a.Tk, blockIdx.x / a.H, n, block)) return;
     const Seq s = attn_seq(a, n);
+    const Reads reads(lane);
     const int key = block * A_ROWS + 32 * w + (lane & 31);
     const int use = min(key, s.lk - 1);
     const int shift = s.lk - s.lq;                          // row i sees keys up to i + shift
@@ -443,25 +483,38 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
     auto load_rows = [&](int tile, int buf) {
         const int64_t first = (int64_t)tile * A_TILE, last = s.lq - 1;
         const uint16_t* q = a.q + s.q0 * a.qt + h * a.qh;
-        copy256(q, first, last, (uint32_t)a.qt * 2, qn0 + buf * A_TILE * 256, w, lane);
-        copy128(q + AN, first, last, (uint32_t)a.qt * 2, qr0 + buf * A_TILE * 128, w, lane);
-        copy256(a.d_o + ((size_t)s.q0 * a.H + h) * AV, first, last, (uint32_t)a.H * AV * 2, td0 + buf * A_TILE * 256, w, lane);
-        if (w < 2) {
-            // wave 0: lse, so that a row behind the end or without keys has weights of zero; wave 1: delta
-            const int64_t r = first + lane;
-            const size_t at = (size_t)(s.q0 + min(r, last)) * a.H + h;
-            float x = w == 0 ? a.lse[at] * LOG2E : a.delta[at];
-            if (w == 0 && (r > last || x == -INFINITY)) x = INFINITY;
-            stat[buf][w][lane] = x;
-        }
+        copy256<4>(q, first, last, (uint32_t)a.qt * 2, qn0 + buf * A_TILE * 256, w, lane);
+        copy128<4>(q + AN, first, last, (uint32_t)a.qt * 2, qr0 + buf * A_TILE * 128, w, lane);
+        copy256<4>(a.d_o + ((size_t)s.q0 * a.H + h) * AV, first, last, (uint32_t)a.H * AV * 2, td0 + buf * A_TILE * 256, w, lane);
+    };
+    // wave 0: lse, so that a row behind the end or without keys has weights of zero; wave 1: delta.  Loaded a
+    // tile before it is put into LDS: a value needed at once would be waited for behind the copies.
+    auto load_stat = [&](int tile) {
+        if (w >= 2) return 0.f;
+        const int64_t r = (int64_t)tile * A_TILE + lane;
+        const size_t at = (size_t)(s.q0 + min(r, (int64_t)s.lq - 1)) * a.H + h;
+        return w == 0 ? (r < s.lq ? a.lse[at] : INFINITY) : a.delta[at];
+    };
+    auto put_stat = [&](float x, int buf) {
+        if (w < 2) stat[buf][w][lane] = w == 0 ? (x == -INFINITY ? INFINITY : x * LOG2E) : x;
     };
 
-    if (j0 < tiles) load_rows(j0, 0);
+    float ahead = 0.f;
+    if (j0 < tiles) {
+        put_stat(load_stat(j0), 0);
+        ahead = load_stat(j0 + 1);   // a tile behind the end reads the last row, and is not used
+        load_rows(j0, 0);
+    }
     for (int j = j0; j < tiles; ++j) {
         const int buf = (j - j0) & 1;
         dma_wait();
         __syncthreads();
-        if (j + 1 < tiles) load_rows(j + 1, buf ^ 1);
+        if (j + 1 < tiles) {
+            put_stat(ahead, buf ^ 1);
+            ahead = load_stat(j + 2);
+            load_rows(j + 1, buf ^ 1);
+        }
+        const Reads x = reads.again();
         const char* tn = qn + buf * A_TILE * 256;
         const char* tr = qr + buf * A_TILE * 128;
         const char* to = td + buf * A_TILE * 256;
@@ -471,11 +524,11 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
             if (r0 + 31 + shift < block * A_ROWS + 32 * w) continue;   // no row here sees these keys
             f32x16 sc = zero16(), dp = zero16();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sc = mma(row256(tn, t, k, lane), kf[k], sc);
+            for (int k = 0; k < 8; ++k) sc = mma(x.row256(tn, t, k), kf[k], sc);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sc = mma(row128(tr, t, k, lane), kf[8 + k], sc);
+            for (int k = 0; k < 4; ++k) sc = mma(x.row128(tr, t, k), kf[8 + k], sc);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dp = mma(row256(to, t, k, lane), vf[k], dp);
+            for (int k = 0; k < 8; ++k) dp = mma(x.row256(to, t, k), vf[k], dp);
             // a key behind the sequence's end is computed like its last and not stored
             const bool cut = r0 + shift < block * A_ROWS + 32 * w + 31;
 #pragma unroll
@@ -495,11 +548,11 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
             for (int u = 0; u < 2; ++u) {
                 const bf16x8 p = operand(sc, u), d = operand(dp, u);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) dv[c] = mma(col256(to, 2 * t + u, c, lane), p, dv[c]);
+                for (int c = 0; c < 4; ++c) dv[c] = mma(x.col256(to, 2 * t + u, c), p, dv[c]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) dk[c] = mma(col256(tn, 2 * t + u, c, lane), d, dk[c]);
+                for (int c = 0; c < 4; ++c) dk[c] = mma(x.col256(tn, 2 * t + u, c), d, dk[c]);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) dk[4 + c] = mma(col128(tr, 2 * t + u, c, lane), d, dk[4 + c]);
+                for (int c = 0; c < 2; ++c) dk[4 + c] = mma(x.col128(tr, 2 * t + u, c), d, dk[4 + c]);
             }
         }
     }
@@ -538,8 +591,8 @@ __global__ __launch_bounds__(256) void latent_dkr_kernel(const float* part, uint
 int64_t total_q(const cdr_latent_attn_problem* p) { return p->varlen ? p->T : (int64_t)p->N * p->T; }
 int64_t total_k(const cdr_latent_attn_problem* p) { return p->varlen ? p->Tk : (int64_t)p->N * p->Tk; }
 
-int64_t attn_slots(int64_t T, const cdr_latent_attn_problem* p) {
-    return p->varlen ? T / A_ROWS + p->N : p->N * ((T + A_ROWS - 1) / A_ROWS);
+int64_t attn_slots(int64_t T, const cdr_latent_attn_problem* p, int rows = A_ROWS) {
+    return p->varlen ? T / rows + p->N : p->N * ((T + rows - 1) / rows);
 }
 
 bool ok_stride(int64_t s) { return s >= 0 && (s & 7) == 0 && s < (1 << 23); }
@@ -641,7 +694,8 @@ cdr_status cdr_latent_attn_bwd(const cdr_latent_attn_problem* p, const void* q, 
         hipLaunchKernelGGL(cdr::latent_delta_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a,
                            static_cast<const uint16_t*>(o));
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
-        hipLaunchKernelGGL(cdr::latent_dq_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a);
+        a.slots = (int)cdr::attn_slots(p->T, p, cdr::DQ_ROWS);
+        hipLaunchKernelGGL(cdr::latent_dq_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(2 * cdr::DQ_ROWS), 0, s, a);
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
     }
     if (tk > 0) {
