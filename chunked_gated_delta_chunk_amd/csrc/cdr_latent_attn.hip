@@ -63,13 +63,19 @@ struct Seq {
     int lq, lk;
 };
 
+// an offset at an index that the whole wave shares, through the scalar cache
+__device__ __forceinline__ int offset_at(const int32_t* cu, int i) {
+    typedef const int32_t __attribute__((address_space(4))) cint32;
+    return ((const cint32*)cu)[i];
+}
+
 __device__ __forceinline__ Seq attn_seq(const LatentAttnArgs& a, int n) {
     Seq s;
     if (a.cuq) {
-        const int qb = min(max(a.cuq[n], 0), a.T), kb = min(max(a.cuk[n], 0), a.Tk);
+        const int qb = min(max(offset_at(a.cuq, n), 0), a.T), kb = min(max(offset_at(a.cuk, n), 0), a.Tk);
         s.q0 = qb, s.k0 = kb;
-        s.lq = min(max(a.cuq[n + 1], qb), a.T) - qb;
-        s.lk = min(max(a.cuk[n + 1], kb), a.Tk) - kb;
+        s.lq = min(max(offset_at(a.cuq, n + 1), qb), a.T) - qb;
+        s.lk = min(max(offset_at(a.cuk, n + 1), kb), a.Tk) - kb;
     } else {
         s.q0 = (int64_t)n * a.T, s.k0 = (int64_t)n * a.Tk;
         s.lq = a.T, s.lk = a.Tk;
@@ -90,12 +96,12 @@ __device__ __forceinline__ bool attn_slot(const LatentAttnArgs& a, const int32_t
     int lo = 0, hi = a.N - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (min(max(cu[mid], 0), T) / ROWS + mid <= slot) lo = mid; else hi = mid - 1;
+        if (min(max(offset_at(cu, mid), 0), T) / ROWS + mid <= slot) lo = mid; else hi = mid - 1;
     }
     n = lo;
-    const int b = min(max(cu[n], 0), T);
+    const int b = min(max(offset_at(cu, n), 0), T);
     block = slot - (b / ROWS + n);
-    return block >= 0 && block * ROWS < min(max(cu[n + 1], b), T) - b;
+    return block >= 0 && block * ROWS < min(max(offset_at(cu, n + 1), b), T) - b;
 }
 
 // Copies rows `first` .. + 63 (clipped to `last`) of an array with 256-byte or 128-byte rows to LDS:
