@@ -397,6 +397,7 @@ __device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, con
             }
         }
     }
+    if constexpr (!DELTA) dma_wait();   // rows without keys: the copy of do is still under way
     const size_t out = (size_t)(s.q0 + row) * a.H + h;
     if constexpr (DELTA) {
         delta += __shfl_xor(delta, 32, 64);
@@ -451,6 +452,8 @@ __global__ __launch_bounds__(256, 2) void latent_delta_kernel(LatentAttnArgs a, 
 
 __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
     __shared__ __align__(256) char lds[A_LDS];
+    __shared__ __align__(256) char own[A_ROWS * (256 + 128)];   // this block's keys, 32 a wave: operands like v's,
+                                                               // for which the registers do not reach
     __shared__ __align__(16) float stat[2][2][A_TILE];   // lse (base 2) and delta of a tile's rows
     char* qn = lds;
     char* qr = qn + 2 * A_TILE * 256;
@@ -468,15 +471,21 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
     const int first_row = max(0, block * A_ROWS - shift);   // the first row that sees a key of this block
     const int j0 = first_row / A_TILE, tiles = (s.lq + A_TILE - 1) / A_TILE;
 
-    bf16x8 kf[12], vf[8];
+    const char* kn = own + w * 32 * 256;
+    const char* kr = own + A_ROWS * 256 + w * 32 * 128;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 4), at = min(block * A_ROWS + 32 * w + r, s.lk - 1);
+        dma16(a.k + (s.k0 + at) * a.kt + h * a.kh + ((lane & 15) ^ f16(r)) * 8, lds_offset(kn) + 1024 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 3), at = min(block * A_ROWS + 32 * w + r, s.lk - 1);
+        dma16(a.kr + (s.k0 + at) * a.rt + ((lane & 7) ^ f8(r)) * 8, lds_offset(kr) + 1024 * i);
+    }
+    bf16x8 vf[8];
     {
-        const uint16_t* k = a.k + (s.k0 + use) * a.kt + h * a.kh + 8 * (lane >> 5);
-        const uint16_t* r = a.kr + (s.k0 + use) * a.rt + 8 * (lane >> 5);
         const uint16_t* v = a.v + (s.k0 + use) * a.vt + h * a.vh + 8 * (lane >> 5);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) kf[i] = *reinterpret_cast<const bf16x8*>(k + 16 * i);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) kf[8 + i] = *reinterpret_cast<const bf16x8*>(r + 16 * i);
 #pragma unroll
         for (int i = 0; i < 8; ++i) vf[i] = *reinterpret_cast<const bf16x8*>(v + 16 * i);
     }
@@ -511,8 +520,8 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
         ahead = load_stat(j0 + 1);   // a tile behind the end reads the last row, and is not used
         load_rows(j0, 0);
     }
-    for (int j = j0; j < tiles; ++j) {
-        const int buf = (j - j0) & 1;
+    // a tile's begin: it has arrived, the next one is sent for
+    auto arrive = [&](int j, int buf) {
         dma_wait();
         __syncthreads();
         if (j + 1 < tiles) {
@@ -520,6 +529,14 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
             ahead = load_stat(j + 2);
             load_rows(j + 1, buf ^ 1);
         }
+    };
+    // Two loops, the tiles whose rows do not all see this wave's keys (they come first) and the others: as
+    // branches of one loop, the sums were copied between registers at every turn.  The waves leave the
+    // first at different tiles; each tile has one barrier in either.
+    int j = j0;
+    for (; j < tiles && j * A_TILE + shift < block * A_ROWS + 32 * w + 31; ++j) {
+        const int buf = (j - j0) & 1;
+        arrive(j, buf);
         const Reads x = reads.again();
         const char* tn = qn + buf * A_TILE * 256;
         const char* tr = qr + buf * A_TILE * 128;
@@ -529,12 +546,30 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
             const int r0 = j * A_TILE + 32 * t;
             if (r0 + 31 + shift < block * A_ROWS + 32 * w) continue;   // no row here sees these keys
             f32x16 sc = zero16(), dp = zero16();
+            // scores and do v^T side by side, two steps' rows read ahead
+            bf16x8 f[2][2], g[2][2], kf[2][2];
+            auto read_rows = [&](int batch) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sc = mma(x.row256(tn, t, k), kf[k], sc);
+                for (int i = 0; i < 2; ++i) {
+                    const int k = 2 * batch + i;
+                    f[batch & 1][i] = k < 8 ? x.row256(tn, t, k) : x.row128(tr, t, k - 8);
+                    kf[batch & 1][i] = k < 8 ? x.row256(kn, 0, k) : x.row128(kr, 0, k - 8);
+                    if (k < 8) g[batch & 1][i] = x.row256(to, t, k);
+                }
+            };
+            read_rows(0);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sc = mma(x.row128(tr, t, k), kf[8 + k], sc);
+            for (int batch = 0; batch < 6; ++batch) {
+                if (batch < 5) read_rows(batch + 1);
+                keep_order();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dp = mma(x.row256(to, t, k), vf[k], dp);
+                for (int i = 0; i < 2; ++i) {
+                    const int k = 2 * batch + i;
+                    sc = mma(f[batch & 1][i], kf[batch & 1][i], sc);
+                    if (k < 8) dp = mma(g[batch & 1][i], vf[k], dp);
+                }
+                keep_order();
+            }
             // a key behind the sequence's end is computed like its last and not stored
             const bool cut = r0 + shift < block * A_ROWS + 32 * w + 31;
 #pragma unroll
@@ -562,6 +597,81 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
             }
         }
     }
+    for (; j < tiles; ++j) {
+        const int buf = (j - j0) & 1;
+        arrive(j, buf);
+        const Reads x = reads.again();
+        const char* tn = qn + buf * A_TILE * 256;
+        const char* tr = qr + buf * A_TILE * 128;
+        const char* to = td + buf * A_TILE * 256;
+        // Every row sees every key.  A wave issues in order, and it is alone on its SIMD: what it computes besides
+        // the products is put between them, one element's weight behind each, so that it costs no time of its own.
+        f32x16 sc[2] = {zero16(), zero16()}, dp[2] = {zero16(), zero16()};
+        f32x4 ls[2], de[2];   // of four rows, and the next four's
+        auto read_stat = [&](int t, int g) {
+            ls[g & 1] = *reinterpret_cast<const f32x4*>(&stat[buf][0][32 * t + 8 * g + 4 * (lane >> 5)]);
+            de[g & 1] = *reinterpret_cast<const f32x4*>(&stat[buf][1][32 * t + 8 * g + 4 * (lane >> 5)]);
+        };
+        auto weight = [&](int t, int i) {
+            if ((i & 3) == 0 && i < 12) read_stat(t, (i >> 2) + 1);
+            const float p = ex2(sc[t][i] * a.scale2 - ls[(i >> 2) & 1][i & 3]);
+            sc[t][i] = p;
+            dp[t][i] = p * (dp[t][i] - de[(i >> 2) & 1][i & 3]);
+        };
+        bf16x8 f[3], g[3], kf[3];   // rows and keys of three steps: two ahead
+        auto read_rows = [&](int t, int k) {
+            f[k % 3] = k < 8 ? x.row256(tn, t, k) : x.row128(tr, t, k - 8);
+            kf[k % 3] = k < 8 ? x.row256(kn, 0, k) : x.row128(kr, 0, k - 8);
+            if (k < 8) g[k % 3] = x.row256(to, t, k);
+        };
+        read_stat(0, 0);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            read_rows(t, 0);
+            read_rows(t, 1);
+            keep_order();
+#pragma unroll
+            for (int k = 0; k < 12; ++k) {
+                if (k < 10) read_rows(t, k + 2);
+                sc[t] = mma(f[k % 3], kf[k % 3], sc[t]);
+                // the twenty products carry sixteen weights: k and k + 1 where there are two products
+                const int i = k < 4 ? 2 * k : k + 4;
+                if (t == 1) weight(0, i);
+                keep_order();
+                if (k < 8) {
+                    dp[t] = mma(g[k % 3], vf[k], dp[t]);
+                    if (t == 1 && k < 4) weight(0, i + 1);
+                    keep_order();
+                }
+            }
+        }
+        bf16x8 c[4];   // column operands: three ahead
+        auto read_columns = [&](int y) {   // dv's four column tiles and dk's six, of each 16 rows
+            const int at = y / 10, z = y % 10;
+            c[y % 4] = z < 4 ? x.col256(to, at, z) : z < 8 ? x.col256(tn, at, z - 4) : x.col128(tr, at, z - 8);
+        };
+        read_stat(1, 0);
+        bf16x8 p[2], d[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) p[u] = operand(sc[0], u), d[u] = operand(dp[0], u);
+        read_columns(0);
+        read_columns(1);
+        read_columns(2);
+        keep_order();
+#pragma unroll
+        for (int y = 0; y < 40; ++y) {
+            const int u = (y / 10) & 1, z = y % 10;
+            if (y < 37) read_columns(y + 3);
+            if (z < 4) dv[z] = mma(c[y % 4], p[u], dv[z]);
+            else dk[z - 4] = mma(c[y % 4], d[u], dk[z - 4]);
+            if (y < 16) weight(1, y);
+            keep_order();
+            if (y == 19)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) p[v] = operand(sc[1], v), d[v] = operand(dp[1], v);
+        }
+    }
+    dma_wait();   // where no row sees these keys, their copies are still under way
     if (key >= s.lk) return;
     const size_t out = (size_t)(s.k0 + key) * a.H + h;
     const int c4 = 4 * (lane >> 5);
