@@ -35,7 +35,7 @@ constexpr int AN = 128;       // nope dimensions
 constexpr int AV = 128;       // value dimensions
 constexpr int AQ = AN + LR;   // a query's
 constexpr int A_ROWS = 128;   // rows (or keys) of a workgroup
-constexpr int DQ_ROWS = 256;  // rows of a workgroup of the dq kernel
+constexpr int A_CUS = 256;
 constexpr int A_TILE = 64;    // rows of a streamed tile
 constexpr int A_LDS = 2 * A_TILE * (256 + 128 + 256);   // two tiles of 320 dimensions
 
@@ -55,6 +55,7 @@ struct LatentAttnArgs {
     float* dkr;         // [H][Tk total][64]
     int64_t qt, qh, kt, kh, rt, vt, vh;   // strides, elements
     int T, Tk, H, N, slots, total_k;
+    int ranked;         // blocks by weight rather than by slot
     float scale, scale2;
 };
 
@@ -102,6 +103,44 @@ __device__ __forceinline__ bool attn_slot(const LatentAttnArgs& a, const int32_t
     const int b = min(max(offset_at(cu, n), 0), T);
     block = slot - (b / ROWS + n);
     return block >= 0 && block * ROWS < min(max(offset_at(cu, n + 1), b), T) - b;
+}
+
+// The same for the WORK-th heaviest block first: of up to 64 packed sequences, all last blocks of the longest,
+// then those a block shorter and so on (FIRST: all first blocks, then all second ones).  With few blocks
+// for each CU the device otherwise ends with a long sequence's heavy blocks alone: 5 sequences of 8168
+// tokens, 16 heads, 127 us in the slots' order and 104 us in this one.
+template <int ROWS, bool FIRST>
+__device__ __forceinline__ bool attn_ranked(const LatentAttnArgs& a, const int32_t* cu, int T, int rank, int& n, int& block) {
+    const int lane = threadIdx.x & 63;
+    int blocks = 0;
+    if (lane < a.N) {
+        const int b = min(max(cu[lane], 0), T);
+        blocks = (min(max(cu[lane + 1], b), T) - b + ROWS - 1) / ROWS;
+    }
+    int most = blocks;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) most = max(most, __shfl_xor(most, m, 64));
+    most = __builtin_amdgcn_readfirstlane(most);
+    for (int i = 0; i < most; ++i) {
+        const int b = FIRST ? i : most - 1 - i;
+        uint64_t with = __ballot(blocks > b);
+        const int count = __popcll(with);
+        if (rank < count) {
+            for (; rank > 0; --rank) with &= with - 1;
+            n = __builtin_ctzll(with);
+            block = b;
+            return true;
+        }
+        rank -= count;
+    }
+    return false;
+}
+
+// The block of a workgroup: heaviest first.
+template <int ROWS, bool FIRST>
+__device__ __forceinline__ bool attn_block(const LatentAttnArgs& a, const int32_t* cu, int T, int i, int& n, int& block) {
+    if (a.ranked) return attn_ranked<ROWS, FIRST>(a, cu, T, i, n, block);
+    return attn_slot<ROWS>(a, cu, T, FIRST ? i : a.slots - 1 - i, n, block);
 }
 
 // Copies rows `first` .. + 63 (clipped to `last`) of an array with 256-byte or 128-byte rows to LDS:
@@ -200,7 +239,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = blockIdx.x % a.H;
     int n, block;
-    if (!attn_slot<A_ROWS>(a, a.cuq, a.T, a.slots - 1 - blockIdx.x / a.H, n, block)) return;
+    if (!attn_block<A_ROWS, false>(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;
     const Seq s = attn_seq(a, n);
     const Tiles at = {lds_offset(kn), lds_offset(kr), lds_offset(vt)};
     const Reads reads(lane);
@@ -411,12 +450,15 @@ __device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, con
         for (int g = 0; g < 4; ++g) put4(a.o + out * AQ + 32 * c + 8 * g + 4 * (lane >> 5), dq[c], g, a.scale);
 }
 
-__global__ __launch_bounds__(2 * DQ_ROWS, 2) void latent_dq_kernel(LatentAttnArgs a) {
-    __shared__ __align__(256) char lds[A_LDS + DQ_ROWS * 256];
+// Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than the CUs, and a block's own
+// time is what counts.
+template <int ROWS>
+__global__ __launch_bounds__(2 * ROWS, 2) void latent_dq_kernel(LatentAttnArgs a) {
+    __shared__ __align__(256) char lds[A_LDS + ROWS * 256];
     const int h = blockIdx.x % a.H;
     int n, block;
-    if (!attn_slot<DQ_ROWS>(a, a.cuq, a.T, a.slots - 1 - blockIdx.x / a.H, n, block)) return;
-    dq_block<false, DQ_ROWS / 32>(a, lds, attn_seq(a, n), h, block);
+    if (!attn_block<ROWS, false>(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;
+    dq_block<false, ROWS / 32>(a, lds, attn_seq(a, n), h, block);
 }
 
 // delta of a block of 128 rows: do . o from the forward's o, 16 lanes a row; but where the rows see at most 128
@@ -462,7 +504,7 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = blockIdx.x % a.H;
     int n, block;
-    if (!attn_slot<A_ROWS>(a, a.cuk, a.Tk, blockIdx.x / a.H, n, block)) return;
+    if (!attn_block<A_ROWS, true>(a, a.cuk, a.Tk, blockIdx.x / a.H, n, block)) return;
     const Seq s = attn_seq(a, n);
     const Reads reads(lane);
     const int key = block * A_ROWS + 32 * w + (lane & 31);
@@ -711,6 +753,14 @@ int64_t attn_slots(int64_t T, const cdr_latent_attn_problem* p, int rows = A_ROW
     return p->varlen ? T / rows + p->N : p->N * ((T + rows - 1) / rows);
 }
 
+// Slots of a launch, and whether its blocks are taken by weight: of 2 to 64 packed sequences with at most
+// sixteen blocks a CU.  With more the last ones are a small part, and finding a block costs steps in the
+// number of blocks a sequence has.
+void set_order(LatentAttnArgs& a, const cdr_latent_attn_problem* p, int64_t slots) {
+    a.slots = (int)slots;
+    a.ranked = p->varlen && p->N >= 2 && p->N <= 64 && slots * p->H <= 16 * A_CUS;
+}
+
 bool ok_stride(int64_t s) { return s >= 0 && (s & 7) == 0 && s < (1 << 23); }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
@@ -770,7 +820,7 @@ cdr_status cdr_latent_attn_fwd(const cdr_latent_attn_problem* p, const void* q, 
     cdr::LatentAttnArgs a = cdr::attn_args(p, q, k_nope, k_rope, v, cu_seqlens, cu_seqlens_k);
     a.o = static_cast<uint16_t*>(o);
     a.lse = lse;
-    a.slots = (int)cdr::attn_slots(p->T, p);
+    cdr::set_order(a, p, cdr::attn_slots(p->T, p));
     hipLaunchKernelGGL(cdr::latent_fwd_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0,
                        static_cast<hipStream_t>(stream), a);
     return hipGetLastError() == hipSuccess ? CDR_OK : CDR_ERR_HIP;
@@ -810,12 +860,15 @@ cdr_status cdr_latent_attn_bwd(const cdr_latent_attn_problem* p, const void* q, 
         hipLaunchKernelGGL(cdr::latent_delta_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a,
                            static_cast<const uint16_t*>(o));
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
-        a.slots = (int)cdr::attn_slots(p->T, p, cdr::DQ_ROWS);
-        hipLaunchKernelGGL(cdr::latent_dq_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(2 * cdr::DQ_ROWS), 0, s, a);
+        const bool large = cdr::attn_slots(p->T, p, 256) * p->H >= cdr::A_CUS;
+        cdr::set_order(a, p, cdr::attn_slots(p->T, p, large ? 256 : 128));
+        const dim3 grid((unsigned)(a.slots * (int64_t)a.H));
+        if (large) hipLaunchKernelGGL((cdr::latent_dq_kernel<256>), grid, dim3(512), 0, s, a);
+        else hipLaunchKernelGGL((cdr::latent_dq_kernel<128>), grid, dim3(256), 0, s, a);
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
     }
     if (tk > 0) {
-        a.slots = (int)cdr::attn_slots(p->Tk, p);
+        cdr::set_order(a, p, cdr::attn_slots(p->Tk, p));
         hipLaunchKernelGGL(cdr::latent_dkv_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a);
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
         hipLaunchKernelGGL(cdr::latent_dkr_kernel, dim3((unsigned)((tk * (cdr::LR / 4) + 255) / 256)), dim3(256), 0, s, a.dkr,
