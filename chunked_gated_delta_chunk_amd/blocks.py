@@ -35,6 +35,16 @@ def _launch(device, what, entry, *args):
         _raise(st, what)
 
 
+def _apart(inputs, outputs):
+    """Raises where an output's memory overlaps an input's (both dicts of dense tensors)."""
+    for n, o in outputs.items():
+        a, size = o.data_ptr(), o.numel() * o.element_size()
+        for m, i in inputs.items():
+            b = i.data_ptr()
+            if a < b + i.numel() * i.element_size() and b < a + size:
+                raise ValueError(f"{n} overlaps {m}, which is read after it is written")
+
+
 def _need_gpu(device):
     if device.type != "cuda":
         raise ValueError("inputs must be on a GPU device")
@@ -249,7 +259,8 @@ def build_page_tables(query_lens: torch.Tensor, context_lens: torch.Tensor, bloc
     place unless ``free_head_out`` is given.  ``max_tokens`` is the size of the token arrays (a
     captured step's): positions and slots behind the last request are 0 and -1.  Nothing is read
     back to the host; ``shortage`` says how many pages were missing.  ``out`` reuses the tensors of
-    an earlier call, as a captured graph does (``free_head`` of it is ignored).
+    an earlier call, as a captured graph does (``free_head`` of it is ignored); they must not overlap
+    the inputs, so an earlier call's ``seq_lens`` taken as ``context_lens`` is not also this call's.
     """
     lib = load_library()
     _need(query_lens, "query_lens", torch.int32)
@@ -281,6 +292,9 @@ def build_page_tables(query_lens: torch.Tensor, context_lens: torch.Tensor, bloc
                            ("shortage", out.shortage, 1)):
             _need(t, "out." + name, torch.int32, (n,), dense=True)
             _on(device, **{"out." + name: t})
+        _apart(dict(query_lens=query_lens, context_lens=context_lens, block_table=block_table, free_pages=free_pages,
+                    free_head=free_head),
+               {"out." + n: t for n, t in zip(out._fields, out) if n != "free_head"})
     _need_gpu(device)
     sizes = [N + 1, N, max_tokens, max_tokens, 1]
     if out is not None:

@@ -15,25 +15,33 @@ from .ops import CDR_OK, _need, _raise, load_library
 LATENT_DIM, LATENT_ROPE = 512, 64
 
 
+_STRIDE_LIMIT = 1 << 23   # elements: the kernels step over a tile's rows in 32 bits
+
+
 def _part(t, name, shape):
-    """A bf16 input read in place where its last dimension is dense, its other strides are
-    multiples of 8 elements and its data is 16-byte aligned; else a contiguous copy."""
+    """A bf16 input read in place where its last dimension is dense, its other strides are multiples
+    of 8 elements and its data is 16-byte aligned; else a contiguous copy.  A stride along a dimension
+    of one element means nothing."""
     _need(t, name, torch.bfloat16, shape)
-    st = t.stride()
-    if t.data_ptr() % 16 or (st[-1] != 1 and t.shape[-1] != 1) or any(s % 8 for s in st[:-1]):
+    odd = t.data_ptr() % 16 or (t.stride(-1) != 1 and t.shape[-1] != 1)
+    if odd or any(n > 1 and (s % 8 or s >= _STRIDE_LIMIT) for s, n in zip(t.stride()[:-1], t.shape)):
         t = t.contiguous()
         if t.data_ptr() % 16:
             t = t.clone()
     return t
 
 
+def _step(t, dim):
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
 def _tokens(t):
     """t ([B, T, ...]) with its first two dimensions as one of packed tokens: (t, token stride)."""
     B, T = t.shape[:2]
-    if B == 1 or T == 0:
-        return t, t.stride(1)
+    if B <= 1 or T == 0:
+        return t, _step(t, 1)
     if T == 1:
-        return t, t.stride(0)
+        return t, _step(t, 0)
     if t.stride(0) != T * t.stride(1):
         t = t.contiguous()
     return t, t.stride(1)
@@ -63,8 +71,8 @@ def latent_cache_write(c: torch.Tensor, k_rope: torch.Tensor, cache: torch.Tenso
     c = _part(c.reshape(T, LATENT_DIM), "c", (T, LATENT_DIM))
     k_rope = _part(k_rope.reshape(T, LATENT_ROPE), "k_rope", (T, LATENT_ROPE))
     slot_map = slot_map.contiguous()
-    _launch(device, "latent_cache_write", lib.cdr_latent_cache_write, T, P, page, _ptr(c), _ptr(k_rope), c.stride(0),
-            k_rope.stride(0), _ptr(cache), _ptr(slot_map))
+    _launch(device, "latent_cache_write", lib.cdr_latent_cache_write, T, P, page, _ptr(c), _ptr(k_rope), _step(c, 0),
+            _step(k_rope, 0), _ptr(cache), _ptr(slot_map))
 
 
 def _check_cache(cache):
@@ -134,8 +142,8 @@ def latent_decode_fwd(q_latent: torch.Tensor, q_rope: torch.Tensor, cache: torch
     qc, qct = _tokens(_part(q_latent, "q_latent", (B, T, H, LATENT_DIM)))
     qr, qrt = _tokens(_part(q_rope, "q_rope", (B, T, H, LATENT_ROPE)))
     p = ops.cdr_latent_decode_problem(N, T, H, int(cu_seqlens is not None), P, page, block_table.shape[1], float(scale))
-    p.qc_stride[0], p.qc_stride[1] = qct, qc.stride(2)
-    p.qr_stride[0], p.qr_stride[1] = qrt, qr.stride(2)
+    p.qc_stride[0], p.qc_stride[1] = qct, _step(qc, 2)
+    p.qr_stride[0], p.qr_stride[1] = qrt, _step(qr, 2)
     ref = ctypes.byref(p)
     st = lib.cdr_latent_decode_check(ref)
     if st != CDR_OK:
@@ -206,9 +214,9 @@ class _LatentAttn:
         self.B, self.T, self.Tk, self.H = B, T, Tk, H
         p = ops.cdr_latent_attn_problem(N, T, Tk, H, int(cu_seqlens is not None),
                                         QUERY_DIM ** -0.5 if scale is None else float(scale))
-        p.q_stride[0], p.q_stride[1] = qt, q.stride(2)
-        p.k_stride[0], p.k_stride[1] = kt, k_nope.stride(2)
-        p.v_stride[0], p.v_stride[1] = vt, v.stride(2)
+        p.q_stride[0], p.q_stride[1] = qt, _step(q, 2)
+        p.k_stride[0], p.k_stride[1] = kt, _step(k_nope, 2)
+        p.v_stride[0], p.v_stride[1] = vt, _step(v, 2)
         p.k_rope_stride = rt
         st = self.lib.cdr_latent_attn_check(ctypes.byref(p))
         if st != CDR_OK:

@@ -408,8 +408,8 @@ cdr_status chunk_dr_recurrent_fwd(const cdr_recurrent_problem* p,
  *                                                   res_scale and gate each optional
  *     h = r * rstd(r) * next_weight                 (has_next)
  *
- * `out` receives r and `next_out` h.  Arithmetic is fp32 whatever the types; h is formed from the
- * fp32 r and each output is rounded once.  With D = 128, a gate, a weight and nothing else this is
+ * `out` receives r and `next_out` h.  Arithmetic is fp32 whatever the types (squares beyond 3e38
+ * overflow); h is formed from the fp32 r and each output is rounded once.  With D = 128, a gate, a weight and nothing else this is
  * the gated norm of o [.., HV, V] per head; with everything it is a whole block boundary.
  *
  *   y, gate      dtype, rows of D contiguous elements (strides below)
@@ -508,7 +508,8 @@ cdr_status cdr_block_norm_bwd(const cdr_block_norm_problem* p, const void* y, co
  * entries other than the new pages' are left as they were.  free_pages[free_head:] is the stack of
  * free pages: a caller gives pages back by writing them below the head and lowering it.
  * shortage[0] counts the pages that were wanted and are not there; a step with a shortage is still
- * well defined (no access leaves the arrays).  free_head_out may be free_head (in place).
+ * well defined (no access leaves the arrays).  free_head_out may be free_head (in place); no other
+ * output may overlap an input.
  *
  *   query_lens, context_lens [N];  block_table [N, table_cols], updated in place
  *   free_pages [num_free];  free_head, free_head_out, shortage [1]
@@ -552,7 +553,8 @@ cdr_status cdr_build_page_tables(int32_t N, int32_t table_cols, int32_t num_free
  *              are left as they were
  *   workspace  at least cdr_latent_decode_workspace_bytes(p) bytes, 16-byte aligned, contents
  *              irrelevant, not to be used by another call until this one's kernels have finished
- * q, cache, o and the workspace are 16-byte aligned.  Scores and sums are fp32; the weights p_j
+ * q, cache, o and the workspace are 16-byte aligned; no output may overlap an input.  Scores and
+ * sums are fp32; the weights p_j
  * enter the second product as bf16 (the first product's sum of them does not).  Lengths are read on
  * the device, so a captured call serves any lengths.  Repeated calls give the same bits.
  * ------------------------------------------------------------------------------------------ */
@@ -618,8 +620,9 @@ cdr_status cdr_latent_cache_write(int32_t T, int32_t num_pages, int32_t page_siz
  * Strides are in elements, multiples of 8, not negative and below 2^23, so k_nope and v may be the
  * two halves of one projection [keys, H, 256]; all but lse are 16-byte aligned.  scale is positive.
  * Values of a sequence must be finite, also those that the causal limit hides from a row (they meet
- * weights of zero); those of other sequences do not matter.  Scores and sums are fp32, the weights
- * enter the second product as bf16.  Repeated calls give the same bits.
+ * weights of zero); those of other sequences do not matter.  No output may overlap an input.
+ * Scores and sums are fp32, the weights enter the second product as bf16.  Repeated calls give the
+ * same bits.
  * ------------------------------------------------------------------------------------------ */
 #define CDR_LATENT_NOPE 128
 #define CDR_LATENT_VALUE 128

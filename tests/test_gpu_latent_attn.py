@@ -160,6 +160,38 @@ def test_layouts_give_the_same():
             assert torch.equal(a, b)
 
 
+def test_strides_of_single_elements_and_far_rows():
+    """One sequence of one token and head with odd strides there; rows further apart than the kernels step."""
+    kw, do = make([1], [1], 1, 40, packed=False)
+    d = {k: v.contiguous().to(DEV) for k, v in kw.items()}
+    want = cdr.latent_attn_fwd(**d)
+    odd = lambda t: torch.as_strided(t, t.shape, (3, 5, 7, 1)[-t.dim():])  # noqa: E731
+    for a, b in zip(cdr.latent_attn_fwd(**{k: odd(v) for k, v in d.items()}), want):
+        assert torch.equal(a, b)
+    kw, do = make([3], [3], 1, 41, packed=False)
+    d = {k: v.contiguous().to(DEV) for k, v in kw.items()}
+    want = cdr.latent_attn_fwd(**d)
+    far = torch.zeros(3 * (1 << 23), dtype=BF16, device=DEV).as_strided((1, 3, 1, 192), (0, 1 << 23, 192, 1))
+    far.copy_(d["q"])
+    for a, b in zip(cdr.latent_attn_fwd(**dict(d, q=far)), want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n", [2, 63, 64, 65])
+def test_many_short_sequences_in_either_order(n):
+    """Up to 64 packed sequences are taken by weight, more by slot."""
+    g = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 40, (n,), generator=g).tolist()
+    lens[n // 2] = 300
+    run(*make(lens, [x + (i % 3) * 50 for i, x in enumerate(lens)], 1, 50 + n))
+
+
+def test_dq_in_blocks_of_either_size():
+    """256 blocks of 256 rows and more take the larger blocks."""
+    kw, do = make([257, 30, 513], [257, 30, 600], 64, 44)
+    run(kw, do)
+
+
 def test_scales_and_large_scores():
     kw, do = make([100], [130], 2, 27)
     run(kw, do, scale=0.4)

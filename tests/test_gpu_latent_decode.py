@@ -149,6 +149,38 @@ def test_strided_queries_and_other_scales():
     run(kw, scale=0.0)
 
 
+def test_a_cache_beyond_32_bit_offsets():
+    """Pages behind 2^31 elements (4.3 GB) of the cache, written and read."""
+    kw = make([200, 33], 1, 16, 64, 19, extra_pages=0)
+    far = 2 ** 31 // (64 * 576) + 5
+    cache = torch.empty(far + kw["cache"].shape[0], 64, 576, dtype=BF16, device=DEV)
+    cache[far:] = kw["cache"].to(DEV)
+    g = dev(kw)
+    table = g["block_table"].clone()
+    table[table < 100] += far
+    o, lse = cdr.latent_decode_fwd(**dict(g, cache=cache, block_table=table), scale=SCALE)
+    compare(kw, o, lse)
+    row = torch.randn(1, 576, generator=torch.Generator().manual_seed(1)).to(BF16).to(DEV)
+    cdr.latent_cache_write(row[:, :512], row[:, 512:], cache,
+                           torch.tensor([far * 64 + 7], dtype=torch.int32, device=DEV))
+    assert torch.equal(cache[far, 7], row[0])
+
+
+def test_strides_of_single_elements_mean_nothing():
+    """One head, one token or one sequence, with strides there that no row could have."""
+    kw = make([40], 1, 1, 16, 18)
+    g = dev(kw)
+    want = cdr.latent_decode_fwd(**g, scale=SCALE)
+    odd = lambda t: torch.as_strided(t, t.shape, (3, 5, 7, 1))  # noqa: E731
+    for a, b in zip(cdr.latent_decode_fwd(**dict(g, q_latent=odd(g["q_latent"]), q_rope=odd(g["q_rope"])), scale=SCALE), want):
+        assert torch.equal(a, b)
+    cache = torch.zeros(1, 16, 576, dtype=BF16, device=DEV)
+    c = torch.as_strided(g["q_latent"].view(512), (1, 512), (3, 1))
+    r = torch.as_strided(g["q_rope"].view(64), (1, 64), (5, 1))
+    cdr.latent_cache_write(c, r, cache, torch.zeros(1, dtype=torch.int32, device=DEV))
+    assert torch.equal(cache[0, 0], torch.cat([c[0], r[0]])) and (cache[0, 1:] == 0).all()
+
+
 def test_large_scores_and_infinite_neighbours():
     """Scores of hundreds (one key carries all), and infinities in rows that no sequence holds."""
     kw = make([90, 64], 1, 16, 16, 13)

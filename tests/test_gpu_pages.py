@@ -91,6 +91,17 @@ def test_head_in_place_and_apart_and_reused_outputs():
     assert got3.slot_map is got2.slot_map
 
 
+def test_outputs_over_inputs_are_refused():
+    """The natural next step, with the last step's lengths as context and its tensors as outputs."""
+    n = 3
+    table, free, head = i32([[-1] * 4] * n), i32(list(range(9))), i32([0])
+    first = cdr.build_page_tables(i32([2] * n), i32([0] * n), table, free, head, 4, 6)
+    with pytest.raises(ValueError, match="overlaps"):
+        cdr.build_page_tables(i32([2] * n), first.seq_lens, table, free, head, 4, 6, out=first)
+    again = cdr.build_page_tables(i32([2] * n), first.seq_lens, table, free, head, 4, 6)
+    assert again.seq_lens.tolist() == [4] * n and again.positions.tolist() == [2, 3] * n
+
+
 def test_graph_replays_advance_the_step():
     """A captured decode step: lengths grow by one and pages come from the list, replay after replay."""
     n, page, cols, cap = 5, 4, 6, 8
