@@ -58,10 +58,17 @@ __device__ __forceinline__ bf16x8 lds16(const void* p) { return *static_cast<con
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
 
-// Where a tile's 16-byte pieces are stored: row `row` keeps piece p at p ^ f(row), f one to one on 16
-// rows.  f16 for rows of a multiple of 256 bytes, f8 for rows of 128 bytes (two of which share 256).
-__device__ __forceinline__ int f16(int row) { return ((row & 7) << 1) | ((row >> 3) & 1); }
-__device__ __forceinline__ int f8(int row) { return (((row >> 1) & 3) << 1) | ((row >> 3) & 1); }
+// Where a tile's 16-byte pieces are stored: row `row` keeps piece p at p ^ f(row).  The 64 banks serve a
+// 16-byte read in four cycles of 16 lanes (lanes 0-3, 12-15, 20-27 together, and so on) and a transposing
+// read in two cycles of 32.  f16, for rows of a multiple of 256 bytes, is one to one on 16 rows and puts
+// four neighbouring rows four pieces apart; f8 does the same for rows of 128 bytes, two of which share
+// 256.  Counted: no conflicts in either read; with neighbours two pieces apart each transposing read took
+// four cycles.  f16w is for the 16-row operands of the decode kernel, where a transposing read takes eight
+// rows of two pieces: one to one, rows 0-7 and 8-15 each two pieces apart, and rows 0-3 and 12-15 in
+// whole pairs of pieces, so that the four pieces of the other lanes' rows stay clear of theirs.
+__device__ __forceinline__ int f16(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
+__device__ __forceinline__ int f8(int row) { return (((row >> 1) & 1) << 2) | ((row >> 2) & 3); }
+__device__ __forceinline__ int f16w(int row) { return (((row & 7) ^ ((row >> 1) & 4)) << 1) | ((row >> 3) & 1); }
 
 // 32x32x16 products: A[m = lane & 31][k = 8 (lane >> 5) + i], B likewise, and the result's register i
 // holds row 8 (i / 4) + 4 (lane >> 5) + i % 4 of column lane & 31.

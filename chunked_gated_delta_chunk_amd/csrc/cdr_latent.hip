@@ -14,7 +14,7 @@
 // 64 keys.
 //  - A tile (72 KiB) goes to LDS once, two deep, by 16-byte copies that need no registers; a key's
 //    latent row is one wave's copy, so its page is looked up in scalar registers.  16-byte pieces
-//    are stored at position p ^ (key & 15), which spreads both reads below over the banks.
+//    are stored at position p ^ f16w(key), which spreads both reads below over the banks.
 //  - Scores: a wave takes 16 or 32 keys against 16 rows, whose q stays in registers as the right
 //    operand, so the result S^T has a row of q in each lane and the running maximum is a lane's own
 //    value after two shuffles and one exchange between the waves.
@@ -206,7 +206,7 @@ __device__ __forceinline__ void dec_load(const LatentDecodeArgs& a, uint32_t kc,
         const uint16_t* base = a.cache + (size_t)__builtin_amdgcn_readlane(row, KPW * w) * LROW;
 #pragma unroll
         for (int i = 0; i < KPW; ++i)
-            dma16(base, (lane16 ^ (((KPW * w + i) & 15) * 16)) + i * (LROW * 2), kc + (KPW * w + i) * (LC * 2));
+            dma16(base, (lane16 ^ (f16w(KPW * w + i) * 16)) + i * (LROW * 2), kc + (KPW * w + i) * (LC * 2));
 #pragma unroll
         for (int i = 0; i < KPW / 8; ++i) {
             const int k = 8 * i + (lane >> 3);
@@ -219,7 +219,7 @@ __device__ __forceinline__ void dec_load(const LatentDecodeArgs& a, uint32_t kc,
         const int key = KPW * w + i;
         const int from = __builtin_amdgcn_readlane(row, key);
         if (from >= 0) {
-            dma16(a.cache + (size_t)from * LROW, lane16 ^ ((key & 15) * 16), kc + key * (LC * 2));
+            dma16(a.cache + (size_t)from * LROW, lane16 ^ (f16w(key) * 16), kc + key * (LC * 2));
         } else {
             *reinterpret_cast<uint4*>(zeros + key * (LC * 2) + lane16) = make_uint4(0, 0, 0, 0);
         }
@@ -260,12 +260,12 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
     // the transposed reads key 4 q + r / 4, the 8 bytes 4 (r & 3) .. of each column tile
     int k_at[4], r_at[2], v_at[CT];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) k_at[k] = (16 * KT * kg + r) * (LC * 2) + ((4 * k + q) ^ r) * 16;
+    for (int k = 0; k < 4; ++k) k_at[k] = (16 * KT * kg + r) * (LC * 2) + ((4 * k + q) ^ f16w(r)) * 16;
 #pragma unroll
     for (int k = 0; k < 2; ++k) r_at[k] = (16 * KT * kg + r) * (LR * 2) + ((4 * k + q) ^ ((r >> 1) & 7)) * 16;
 #pragma unroll
     for (int c = 0; c < CT; ++c)
-        v_at[c] = (4 * q + (r >> 2)) * (LC * 2) + ((2 * (CT * w + c) + ((r >> 1) & 1)) ^ (4 * q + (r >> 2))) * 16 +
+        v_at[c] = (4 * q + (r >> 2)) * (LC * 2) + ((2 * (CT * w + c) + ((r >> 1) & 1)) ^ f16w(4 * q + (r >> 2))) * 16 +
                   (r & 1) * 8;
     while (pos < run.end) {
         Unit u;
@@ -593,7 +593,9 @@ __global__ __launch_bounds__(256) void latent_write_kernel(const uint16_t* c, co
 }
 
 // Rows of a block: the fewest of 16, 32 and 64 that hold the rows of a sequence (of an average one
-// in a packed batch); more rows would be computed for nothing, fewer would read the keys again.
+// in a packed batch); more rows would be computed for nothing, fewer would read the keys again.  64 sequences
+// of up to 4096 keys with blocks of 16, 32 and 64: 16 heads 56, 58 and 65 us, 32 heads 71, 66 and 70, 64
+// heads 109, 82 and 82, 128 heads 178, 106 and 108.
 int dec_m(const cdr_latent_decode_problem* p) {
     const int64_t tokens = p->varlen ? ((int64_t)p->T + p->N - 1) / p->N : p->T;
     const int64_t rows = tokens * p->H;

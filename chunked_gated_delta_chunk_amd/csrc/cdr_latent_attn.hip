@@ -450,8 +450,9 @@ __device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, con
         for (int g = 0; g < 4; ++g) put4(a.o + out * AQ + 32 * c + 8 * g + 4 * (lane >> 5), dq[c], g, a.scale);
 }
 
-// Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than the CUs, and a block's own
-// time is what counts.
+// Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than two a CU, and a block's own
+// time is what counts (4 packed sequences with gradients, 8192 tokens: 16 heads 675 us with 128 and 619 with 256
+// rows, 8 heads 400 and 423; 1001 tokens of 8 heads 64 and 68).
 template <int ROWS>
 __global__ __launch_bounds__(2 * ROWS, 2) void latent_dq_kernel(LatentAttnArgs a) {
     __shared__ __align__(256) char lds[A_LDS + ROWS * 256];
@@ -860,7 +861,7 @@ cdr_status cdr_latent_attn_bwd(const cdr_latent_attn_problem* p, const void* q, 
         hipLaunchKernelGGL(cdr::latent_delta_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a,
                            static_cast<const uint16_t*>(o));
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
-        const bool large = cdr::attn_slots(p->T, p, 256) * p->H >= cdr::A_CUS;
+        const bool large = cdr::attn_slots(p->T, p, 256) * p->H >= 2 * cdr::A_CUS;
         cdr::set_order(a, p, cdr::attn_slots(p->T, p, large ? 256 : 128));
         const dim3 grid((unsigned)(a.slots * (int64_t)a.H));
         if (large) hipLaunchKernelGGL((cdr::latent_dq_kernel<256>), grid, dim3(512), 0, s, a);

@@ -515,7 +515,7 @@ cdr_status cdr_block_norm_bwd(const cdr_block_norm_problem* p, const void* y, co
  *   free_pages [num_free];  free_head, free_head_out, shortage [1]
  *   cu_seqlens [N + 1];  seq_lens [N];  positions, slot_map [max_tokens]
  *   workspace  at least cdr_page_tables_workspace_bytes(N) bytes
- * One kernel is queued for up to 4096 tokens, two beyond.
+ * One kernel is queued for up to 2048 tokens, two beyond.
  * ------------------------------------------------------------------------------------------ */
 size_t cdr_page_tables_workspace_bytes(int32_t N);
 
