@@ -56,6 +56,10 @@ def _on(device, **tensors):
             raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _dense_like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -136,17 +140,15 @@ class _BlockNorm:
         p.alpha, p.eps = alpha, float(eps)
         self.p = p
         self.lib = load_library()
-        st = self.lib.cdr_block_norm_check(ctypes.byref(p))
-        if st != CDR_OK:
-            _raise(st, "block_norm")
         self.y, p.y_stride[0], p.y_stride[1] = _rows(y, p.inner)
         self.gate = self.residual = None
         if gate is not None:
             self.gate, p.gate_stride[0], p.gate_stride[1] = _rows(gate, p.inner)
         if residual is not None:
             self.residual, p.residual_stride[0], p.residual_stride[1] = _rows(residual, p.inner)
-        dense = lambda t: None if t is None else t.contiguous()  # noqa: E731
-        self.weight, self.scale, self.next_weight = dense(weight), dense(res_scale), dense(next_weight)
+        self.weight = None if weight is None else weight.contiguous()
+        self.scale = None if res_scale is None else res_scale.contiguous()
+        self.next_weight = None if next_weight is None else next_weight.contiguous()
         self.inputs = (_ptr(self.y), _ptr(self.gate), _ptr(self.residual), _ptr(self.weight), _ptr(self.scale),
                        _ptr(self.next_weight))
 
@@ -182,9 +184,9 @@ def block_norm_fwd(y: torch.Tensor, weight: Optional[torch.Tensor] = None,
     _on(c.device, out=out, next_out=next_out)
     _need_gpu(c.device)
     if out is None:
-        out = torch.empty(c.shape, dtype=c.out_dtype, device=c.device)
+        out = _dense_like(y if residual is None else residual)
     if next_out is None and next_weight is not None:
-        next_out = torch.empty(c.shape, dtype=c.dtype, device=c.device)
+        next_out = _dense_like(y)
     _launch(c.device, "block_norm_fwd", c.lib.cdr_block_norm_fwd, ctypes.byref(c.p), *c.inputs, out.data_ptr(),
             _ptr(next_out))
     return out, next_out
@@ -222,14 +224,11 @@ def block_norm_bwd(y: torch.Tensor, d_out: Optional[torch.Tensor], d_next: Optio
         raise ValueError("workspace too small")
     elif not workspace.is_contiguous() or workspace.data_ptr() % 16:
         raise ValueError("workspace must be contiguous and 16-byte aligned")
-    empty = lambda dtype: torch.empty(c.shape, dtype=dtype, device=c.device)  # noqa: E731
-    vec = lambda t: None if t is None else torch.empty(c.D, dtype=torch.float32, device=c.device)  # noqa: E731
+    like = lambda t: None if t is None else _dense_like(t)  # noqa: E731
     dense = lambda t: None if t is None else t.contiguous()  # noqa: E731
     d_out, d_next = dense(d_out), dense(d_next)
-    dy = empty(c.dtype)
-    dgate = empty(c.dtype) if gate is not None else None
-    dres = empty(c.out_dtype) if residual is not None else None
-    dw, ds, dw2 = vec(c.weight), vec(c.scale), vec(c.next_weight)
+    dy, dgate, dres = _dense_like(y), like(gate), like(residual)
+    dw, ds, dw2 = like(c.weight), like(c.scale), like(c.next_weight)
     _launch(c.device, "block_norm_bwd", c.lib.cdr_block_norm_bwd, ctypes.byref(c.p), *c.inputs, _ptr(d_out),
             _ptr(d_next), _ptr(dy), _ptr(dgate), _ptr(dres), _ptr(dw), _ptr(ds), _ptr(dw2), _ptr(workspace),
             workspace.numel() * workspace.element_size())
@@ -300,10 +299,10 @@ def build_page_tables(query_lens: torch.Tensor, context_lens: torch.Tensor, bloc
     if out is not None:
         cu, lens, pos, slot, short = out.cu_seqlens, out.seq_lens, out.positions, out.slot_map, out.shortage
     elif workspace is not None:
-        cu, lens, pos, slot, short = torch.empty(sum(sizes), dtype=torch.int32, device=device).split(sizes)
+        cu, lens, pos, slot, short = torch.empty(sum(sizes), dtype=torch.int32, device=device).split_with_sizes(sizes)
     else:   # one allocation, the scratch space at its end
         sizes.append(need // 4)
-        cu, lens, pos, slot, short, workspace = torch.empty(sum(sizes), dtype=torch.int32, device=device).split(sizes)
+        cu, lens, pos, slot, short, workspace = torch.empty(sum(sizes), dtype=torch.int32, device=device).split_with_sizes(sizes)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
     elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous() \

@@ -23,6 +23,8 @@ def _part(t, name, shape):
     of 8 elements and its data is 16-byte aligned; else a contiguous copy.  A stride along a dimension
     of one element means nothing."""
     _need(t, name, torch.bfloat16, shape)
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t
     odd = t.data_ptr() % 16 or (t.stride(-1) != 1 and t.shape[-1] != 1)
     if odd or any(n > 1 and (s % 8 or s >= _STRIDE_LIMIT) for s, n in zip(t.stride()[:-1], t.shape)):
         t = t.contiguous()
