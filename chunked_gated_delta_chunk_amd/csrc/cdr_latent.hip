@@ -493,7 +493,7 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
 // workgroup wg's run.  A unit of many parts (one long sequence over the whole device) takes a workgroup
 // for each row, whose eight waves take every eighth part; one of few parts a wave for each row, and
 // every eighth workgroup for eight rows.  (A workgroup a row for two parts each took 26 us for 256 units of
-// 64 rows, a wave a row 13 us; a wave a row for 128 parts would take 40 us where the waves together take 5.)
+// 64 rows, a wave a row 13 us.  The eight waves together take 5.5 to 7 us for 16 rows of 128 parts.)
 constexpr int JOIN_WAVES = 8;
 
 struct Joined {

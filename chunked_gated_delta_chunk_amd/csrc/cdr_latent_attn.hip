@@ -105,10 +105,10 @@ __device__ __forceinline__ bool attn_slot(const LatentAttnArgs& a, const int32_t
     return block >= 0 && block * ROWS < min(max(offset_at(cu, n + 1), b), T) - b;
 }
 
-// The same for the WORK-th heaviest block first: of up to 64 packed sequences, all last blocks of the longest,
-// then those a block shorter and so on (FIRST: all first blocks, then all second ones).  With few blocks
-// for each CU the device otherwise ends with a long sequence's heavy blocks alone: 5 sequences of 8168
-// tokens, 16 heads, 127 us in the slots' order and 104 us in this one.
+// The same with the heaviest blocks first, `rank` counting them: of up to 64 packed sequences, all last blocks
+// of the longest, then those a block shorter and so on (FIRST: all first blocks, then all second ones).  With
+// few blocks for each CU the device otherwise ends with a long sequence's heavy blocks alone: 5 sequences of
+// 8168 tokens, 16 heads, 129 us in the slots' order and 121 us in this one.
 template <int ROWS, bool FIRST>
 __device__ __forceinline__ bool attn_ranked(const LatentAttnArgs& a, const int32_t* cu, int T, int rank, int& n, int& block) {
     const int lane = threadIdx.x & 63;
@@ -454,7 +454,7 @@ __device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, con
 // time is what counts (4 packed sequences with gradients, 8192 tokens: 16 heads 675 us with 128 and 619 with 256
 // rows, 8 heads 400 and 423; 1001 tokens of 8 heads 64 and 68).
 template <int ROWS>
-__global__ __launch_bounds__(2 * ROWS, 2) void latent_dq_kernel(LatentAttnArgs a) {
+__global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kernel(LatentAttnArgs a) {
     __shared__ __align__(256) char lds[A_LDS + ROWS * 256];
     const int h = blockIdx.x % a.H;
     int n, block;
