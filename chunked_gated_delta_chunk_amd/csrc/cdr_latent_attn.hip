@@ -47,7 +47,7 @@ struct LatentAttnArgs {
     const int32_t* cuq;
     const int32_t* cuk;
     const uint16_t* d_o;
-    float* delta;
+    float* delta;       // written by the dq kernel
     uint16_t* o;        // forward: o; dq kernel: dq
     float* lse;
     uint16_t* dk;
@@ -349,12 +349,25 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     if (lane < 32) a.lse[out] = l == 0.f ? -INFINITY : LN2 * (m + lg2(l));
 }
 
-// dq of a block of 32 NW rows, or with DELTA its delta as sum_j p_ij (do_i . v_j): nothing of the loop but the
-// scores and dp then.  For dq a wave holds 48 registers of q and 96 of sums; do, 32 more, stays in LDS (`mine`),
-// without which the loop spilled and each spill's reload waited for the copies under way.
-template <bool DELTA, int NW>
-__device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, const Seq& s, int h, int block) {
-    constexpr int ROWS = 32 * NW;
+// dq of a block of 32 NW rows, and delta on the way.  A wave holds 48 registers of q and 96 of sums; do, 32 more,
+// stays in LDS (`mine`), without which the loop spilled and each spill's reload waited for the copies under way.
+//
+// delta is do . o from the forward's o, but for rows that see at most 128 keys it is summed from the weights.
+// There ds is a difference of two numbers of one size (a row of one key has ds = 0), o is large and its rounding
+// to bf16 would be a tenth of the error of dq and dk; behind many keys o is an average and its rounding counts
+// little.
+//
+// Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than two a CU, and a block's own
+// time is what counts (4 packed sequences with gradients, 8192 tokens: 16 heads 675 us with 128 and 619 with 256
+// rows, 8 heads 400 and 423; 1001 tokens of 8 heads 64 and 68).
+template <int ROWS>
+__global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kernel(LatentAttnArgs a, const uint16_t* o) {
+    constexpr int NW = ROWS / 32;
+    __shared__ __align__(256) char lds[A_LDS + ROWS * 256];
+    const int h = blockIdx.x % a.H;
+    int n, block;
+    if (!attn_block<ROWS, false>(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;
+    const Seq s = attn_seq(a, n);
     char* kn = lds;
     char* kr = kn + 2 * A_TILE * 256;
     char* vt = kr + 2 * A_TILE * 128;
@@ -370,62 +383,102 @@ __device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, con
     const int tiles = keys > 0 ? (keys + A_TILE - 1) / A_TILE : 0;
 
     const size_t in = (size_t)(s.q0 + use) * a.H + h;
-    bf16x8 qf[12], df[DELTA ? 8 : 1];
+    bf16x8 qf[12];
     char* mine = lds + A_LDS + w * 32 * 256;
+    float delta = 0.f;
     {
+        uint4 of[8];
+        const uint16_t* at_o = o + in * AV + 8 * (lane >> 5);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) of[k] = *reinterpret_cast<const uint4*>(at_o + 16 * k);
         const uint16_t* q = a.q + (s.q0 + use) * a.qt + h * a.qh + 8 * (lane >> 5);
 #pragma unroll
         for (int k = 0; k < 12; ++k) qf[k] = *reinterpret_cast<const bf16x8*>(q + 16 * k);
-        if constexpr (DELTA) {
-            const uint16_t* d = a.d_o + in * AV + 8 * (lane >> 5);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) df[k] = *reinterpret_cast<const bf16x8*>(d + 16 * k);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 4 * i + (lane >> 4), at_row = min(block * ROWS + 32 * w + r, s.lq - 1);
-                dma16(a.d_o + ((size_t)(s.q0 + at_row) * a.H + h) * AV + ((lane & 15) ^ f16(r)) * 8, lds_offset(mine) + 1024 * i);
-            }
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 4), at_row = min(block * ROWS + 32 * w + r, s.lq - 1);
+            dma16(a.d_o + ((size_t)(s.q0 + at_row) * a.H + h) * AV + ((lane & 15) ^ f16(r)) * 8, lds_offset(mine) + 1024 * i);
         }
+        if (tiles > 0) load_keys<NW>(a, s, h, 0, 0, at, w, lane);
+        dma_wait();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float x[8], y[8];
+            unpack8(of[k], x);
+            unpack8(__builtin_bit_cast(uint4, reads.row256(mine, 0, k)), y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) delta += x[e] * y[e];
+        }
+        delta += __shfl_xor(delta, 32, 64);
     }
     float lse = a.lse[in] * LOG2E;
     if (lse == -INFINITY) lse = INFINITY;   // a row without keys: all its weights are zero
-    float delta = DELTA ? 0.f : a.delta[in];
-    f32x16 dq[DELTA ? 1 : 6];
-    if constexpr (!DELTA)
-#pragma unroll
-        for (int c = 0; c < 6; ++c) dq[c] = zero16();
 
-    if (tiles > 0) load_keys<NW>(a, s, h, 0, 0, at, w, lane);
+    // s, then do . v, of this lane's row and the 32 keys of half t of tile j, and the weights
+    auto scores = [&](const Reads& x, int j, int t, float (&p)[16], f32x16& dp) {
+        const int buf = j & 1;
+        const char* tn = kn + buf * A_TILE * 256;
+        const char* tr = kr + buf * A_TILE * 128;
+        const char* tv = vt + buf * A_TILE * 256;
+        const Reads again = reads.again();   // do's own reads: not kept from one half to the next
+        f32x16 sc = zero16();
+        dp = zero16();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sc = mma(x.row256(tn, t, k), qf[k], sc);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sc = mma(x.row128(tr, t, k), qf[8 + k], sc);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dp = mma(x.row256(tv, t, k), again.row256(mine, 0, k), dp);
+        const bool cut = j * A_TILE + 32 * t + 32 > lim_first;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            p[i] = ex2(sc[i] * a.scale2 - lse);
+            if (cut && j * A_TILE + 32 * t + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= lim) p[i] = 0.f;
+        }
+    };
+
+    const bool early = s.lk - s.lq + block * ROWS + 1 <= 2 * A_TILE;   // the block's first row at least
+    if (early) {   // leaves both tiles in LDS
+        float sum = 0.f;
+        for (int j = 0; j < min(tiles, 2); ++j) {
+            dma_wait();
+            __syncthreads();
+            if (j == 0 && tiles > 1) load_keys<NW>(a, s, h, 1, 1, at, w, lane);
+            const Reads x = reads.again();
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+                if (j * A_TILE + 32 * t >= lim_last) break;
+                float p[16];
+                f32x16 dp;
+                scores(x, j, t, p, dp);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum += p[i] * dp[i];
+            }
+        }
+        sum += __shfl_xor(sum, 32, 64);
+        if (lim <= 2 * A_TILE) delta = sum;
+    }
+    if (row < s.lq && lane < 32) a.delta[in] = delta;
+
+    f32x16 dq[6];
+#pragma unroll
+    for (int c = 0; c < 6; ++c) dq[c] = zero16();
     for (int j = 0; j < tiles; ++j) {
         const int buf = j & 1;
         dma_wait();
         __syncthreads();
-        if (j + 1 < tiles) load_keys<NW>(a, s, h, j + 1, buf ^ 1, at, w, lane);
+        if (j + 1 < tiles && !(early && j == 0)) load_keys<NW>(a, s, h, j + 1, buf ^ 1, at, w, lane);
         const Reads x = reads.again();
         const char* tn = kn + buf * A_TILE * 256;
         const char* tr = kr + buf * A_TILE * 128;
-        const char* tv = vt + buf * A_TILE * 256;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             if (j * A_TILE + 32 * t >= lim_last) break;
-            const Reads again = reads.again();   // do's own reads: not kept from one half to the next
-            f32x16 sc = zero16(), dp = zero16();
+            float p[16];
+            f32x16 dp;
+            scores(x, j, t, p, dp);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sc = mma(x.row256(tn, t, k), qf[k], sc);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) sc = mma(x.row128(tr, t, k), qf[8 + k], sc);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) dp = mma(x.row256(tv, t, k), DELTA ? df[DELTA ? k : 0] : again.row256(mine, 0, k), dp);
-            const bool cut = j * A_TILE + 32 * t + 32 > lim_first;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float p = ex2(sc[i] * a.scale2 - lse);
-                if (cut && j * A_TILE + 32 * t + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= lim) p = 0.f;
-                if constexpr (DELTA) delta += p * dp[i];
-                else dp[i] = p * (dp[i] - delta);
-            }
-            if constexpr (!DELTA)
+            for (int i = 0; i < 16; ++i) dp[i] = p[i] * (dp[i] - delta);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const bf16x8 d = operand(dp, u);
@@ -436,61 +489,12 @@ __device__ __forceinline__ void dq_block(const LatentAttnArgs& a, char* lds, con
             }
         }
     }
-    if constexpr (!DELTA) dma_wait();   // rows without keys: the copy of do is still under way
-    const size_t out = (size_t)(s.q0 + row) * a.H + h;
-    if constexpr (DELTA) {
-        delta += __shfl_xor(delta, 32, 64);
-        if (row < s.lq && lane < 32) a.delta[out] = delta;
-        return;
-    }
     if (row >= s.lq) return;
+    const size_t out = (size_t)(s.q0 + row) * a.H + h;
 #pragma unroll
     for (int c = 0; c < 6; ++c)
 #pragma unroll
         for (int g = 0; g < 4; ++g) put4(a.o + out * AQ + 32 * c + 8 * g + 4 * (lane >> 5), dq[c], g, a.scale);
-}
-
-// Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than two a CU, and a block's own
-// time is what counts (4 packed sequences with gradients, 8192 tokens: 16 heads 675 us with 128 and 619 with 256
-// rows, 8 heads 400 and 423; 1001 tokens of 8 heads 64 and 68).
-template <int ROWS>
-__global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kernel(LatentAttnArgs a) {
-    __shared__ __align__(256) char lds[A_LDS + ROWS * 256];
-    const int h = blockIdx.x % a.H;
-    int n, block;
-    if (!attn_block<ROWS, false>(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;
-    dq_block<false, ROWS / 32>(a, lds, attn_seq(a, n), h, block);
-}
-
-// delta of a block of 128 rows: do . o from the forward's o, 16 lanes a row; but where the rows see at most 128
-// keys, from the weights themselves.  There ds is a difference of two numbers of one size (a row of one key
-// has ds = 0), o is large and its rounding to bf16 would be a tenth of the error of dq and dk; behind many keys
-// o is an average and its rounding counts little.
-__global__ __launch_bounds__(256, 2) void latent_delta_kernel(LatentAttnArgs a, const uint16_t* o) {
-    __shared__ __align__(256) char lds[A_LDS];
-    const int h = blockIdx.x % a.H;
-    int n, block;
-    if (!attn_slot<A_ROWS>(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;
-    const Seq s = attn_seq(a, n);
-    const int last = min(block * A_ROWS + A_ROWS, s.lq) - 1;
-    if (s.lk - s.lq + last + 1 <= 2 * A_TILE) {
-        dq_block<true, A_ROWS / 32>(a, lds, s, h, block);
-        return;
-    }
-    const int i = threadIdx.x & 15;
-#pragma unroll 4
-    for (int r = 0; r < A_ROWS / 16; ++r) {
-        const int row = block * A_ROWS + 16 * r + (threadIdx.x >> 4);
-        const size_t at = (size_t)(s.q0 + min(row, last)) * a.H + h;
-        float x[8], y[8], t = 0.f;
-        unpack8(*reinterpret_cast<const uint4*>(o + at * AV + 8 * i), x);
-        unpack8(*reinterpret_cast<const uint4*>(a.d_o + at * AV + 8 * i), y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t += x[e] * y[e];
-#pragma unroll
-        for (int k = 1; k < 16; k <<= 1) t += __shfl_xor(t, k, 64);
-        if (row <= last && i == 0) a.delta[at] = t;
-    }
 }
 
 __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
@@ -857,15 +861,12 @@ cdr_status cdr_latent_attn_bwd(const cdr_latent_attn_problem* p, const void* q, 
     a.dk = static_cast<uint16_t*>(dk_nope);
     a.dv = static_cast<uint16_t*>(dv);
     if (tq > 0) {
-        a.slots = (int)cdr::attn_slots(p->T, p);
-        hipLaunchKernelGGL(cdr::latent_delta_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a,
-                           static_cast<const uint16_t*>(o));
-        if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
+        const uint16_t* fo = static_cast<const uint16_t*>(o);
         const bool large = cdr::attn_slots(p->T, p, 256) * p->H >= 2 * cdr::A_CUS;
         cdr::set_order(a, p, cdr::attn_slots(p->T, p, large ? 256 : 128));
         const dim3 grid((unsigned)(a.slots * (int64_t)a.H));
-        if (large) hipLaunchKernelGGL((cdr::latent_dq_kernel<256>), grid, dim3(512), 0, s, a);
-        else hipLaunchKernelGGL((cdr::latent_dq_kernel<128>), grid, dim3(256), 0, s, a);
+        if (large) hipLaunchKernelGGL((cdr::latent_dq_kernel<256>), grid, dim3(512), 0, s, a, fo);
+        else hipLaunchKernelGGL((cdr::latent_dq_kernel<128>), grid, dim3(256), 0, s, a, fo);
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
     }
     if (tk > 0) {
