@@ -358,8 +358,8 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
 // little.
 //
 // Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than two a CU, and a block's own
-// time is what counts (4 packed sequences with gradients, 8192 tokens: 16 heads 675 us with 128 and 619 with 256
-// rows, 8 heads 400 and 423; 1001 tokens of 8 heads 64 and 68).
+// time is what counts (4 packed sequences with gradients, 8192 tokens: 16 heads 666 us with 128 and 615 with 256
+// rows, 8 heads 392 and 417; 1001 tokens of 8 heads 56 and 66).
 template <int ROWS>
 __global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kernel(LatentAttnArgs a, const uint16_t* o) {
     constexpr int NW = ROWS / 32;
