@@ -409,8 +409,9 @@ cdr_status chunk_dr_recurrent_fwd(const cdr_recurrent_problem* p,
  *     h = r * rstd(r) * next_weight                 (has_next)
  *
  * `out` receives r and `next_out` h.  Arithmetic is fp32 whatever the types (squares beyond 3e38
- * overflow); h is formed from the fp32 r and each output is rounded once.  With D = 128, a gate, a weight and nothing else this is
- * the gated norm of o [.., HV, V] per head; with everything it is a whole block boundary.
+ * overflow); h is formed from the fp32 r and each output is rounded once.  With D = 128, a gate, a
+ * weight and nothing else this is the gated norm of o [.., HV, V] per head; with everything it is a
+ * whole block boundary.
  *
  *   y, gate      dtype, rows of D contiguous elements (strides below)
  *   residual     res_dtype, likewise
