@@ -192,6 +192,13 @@ def test_dq_in_blocks_of_either_size():
     run(kw, do)
 
 
+@pytest.mark.parametrize("H", [2, 80])
+def test_rows_on_both_sides_of_128_keys(H):
+    """Blocks of either size in which delta comes from the weights for some rows and from o for others, among
+    them blocks that begin with rows without keys and contexts that end at the border."""
+    run(*make([300, 256, 129, 257], [200, 383, 129, 130], H, 45))
+
+
 def test_scales_and_large_scores():
     kw, do = make([100], [130], 2, 27)
     run(kw, do, scale=0.4)
