@@ -231,9 +231,10 @@ __device__ __forceinline__ void load_keys(const LatentAttnArgs& a, const Seq& s,
     copy256<NW>(a.v + s.k0 * a.vt + h * a.vh, first, last, (uint32_t)a.vt * 2, at.v + buf * A_TILE * 256, w, lane);
 }
 
-// o and lse of a block of 128 rows: two workgroups a CU, so that one's products cover the other's softmax.
-// 8192 tokens, 16 heads: 377 us, 0.91 PFLOP/s, the matrix unit 55 % busy; the softmax's arithmetic, which
-// both workgroups of a SIMD share, and the waits at its ends bound the rest.
+// o and lse of a block of 128 rows: two workgroups a CU, so that one's products cover the other's softmax; a
+// wave is preferred during its products, so that the two stay apart.  8192 tokens, 16 heads: 353 us, 0.97
+// PFLOP/s, the matrix unit 58 % busy; the softmax's arithmetic, which both workgroups of a SIMD share, and the
+// waits at its ends bound the rest.  (Cold: rescaling o at every new maximum and without the preference 348 us, lazily 338, with both 334.)
 __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     __shared__ __align__(256) char lds[A_LDS];
     char* kn = lds;
@@ -289,6 +290,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
                     f[batch & 1][i][t] = k < 8 ? x.row256(tn, t, k) : x.row128(tr, t, k - 8);
                 }
         };
+        __builtin_amdgcn_s_setprio(1);
         read_keys(0);
 #pragma unroll
         for (int batch = 0; batch < 6; ++batch) {
@@ -300,6 +302,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
                 for (int t = 0; t < 2; ++t) sc[t] = mma(f[batch & 1][i][t], qf[2 * batch + i], sc[t]);
             keep_order();
         }
+        __builtin_amdgcn_s_setprio(0);
         if ((j + 1) * A_TILE > lim_first) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -313,7 +316,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[t][i]);
         top = fmaxf(top, __shfl_xor(top, 32, 64)) * a.scale2;
-        const float now = fmaxf(m, top);
+        const float now = top > m + LAZY ? top : m;
         const float ref = now == -INFINITY ? 0.f : now;
         const float alpha = ex2(m - ref);
         m = now;
@@ -332,6 +335,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[c][i] *= alpha;
         }
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -340,6 +344,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[c] = mma(x.col256(tv, 2 * t + u, c), p, o[c]);
             }
+        __builtin_amdgcn_s_setprio(0);
     }
     l += __shfl_xor(l, 32, 64);
     if (row >= s.lq) return;
@@ -362,8 +367,8 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
 //
 // Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than two a CU, and a block's own
 // time is what counts (4 packed sequences with gradients, 8192 tokens: 16 heads 666 us with 128 and 615 with 256
-// rows, 8 heads 392 and 417; 1001 tokens of 8 heads 56 and 66).  8192 tokens, 16 heads: 558 us, the matrix unit
-// 54 % busy, 0.99 PFLOP/s with the scores that it computes again.
+// rows, 8 heads 392 and 417; 1001 tokens of 8 heads 56 and 66).  8192 tokens, 16 heads: 541 us, the matrix unit
+// 55 % busy, 1.02 PFLOP/s with the scores that it computes again.
 template <int ROWS>
 __global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kernel(LatentAttnArgs a, const uint16_t* o) {
     constexpr int NW = ROWS / 32;
@@ -427,12 +432,13 @@ __global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kerne
         const Reads again = reads.again();   // do's own reads: not kept from one half to the next
         f32x16 sc = zero16();
         dp = zero16();
+        // the two sums in turn: of products of one sum each waits for the one before (8192 tokens, 16 heads: 7 us)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sc = mma(x.row256(tn, t, k), qf[k], sc);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc = mma(x.row128(tr, t, k), qf[8 + k], sc);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) dp = mma(x.row256(tv, t, k), again.row256(mine, 0, k), dp);
+        for (int k = 0; k < 8; ++k) {
+            dp = mma(x.row256(tv, t, k), again.row256(mine, 0, k), dp);
+            sc = mma(x.row256(tn, t, k), qf[k], sc);
+            if (k & 1) sc = mma(x.row128(tr, t, k >> 1), qf[8 + (k >> 1)], sc);
+        }
         const bool cut = j * A_TILE + 32 * t + 32 > lim_first;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
