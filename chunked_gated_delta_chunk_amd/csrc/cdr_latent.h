@@ -32,11 +32,6 @@ __device__ __forceinline__ void dma_wait() {
     asm volatile("" ::: "memory");
 }
 
-// The running maximum of a softmax is raised only by more than this (base 2): weights of up to 2^8 are as
-// exact in bf16 and their sums in fp32 as weights of up to 1, and the sums are rescaled a few times in all
-// instead of whenever a row meets a slightly larger score.
-constexpr float LAZY = 8.f;
-
 // Nothing is moved across this.  Between a batch of LDS reads and the products of the batch before
 // it: left alone, the compiler reads one operand, waits and multiplies, one LDS latency a product.
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }

@@ -31,7 +31,7 @@
 // give the same bits.
 //
 // Measured: 256 sequences of up to 8192 keys, 16 heads, 232 us, 5.3 TB/s of cache, which HBM bounds; 64
-// sequences of 4 tokens and 64 heads, up to 4096 keys, 136 us, of which the copies to LDS alone (four row
+// sequences of 4 tokens and 64 heads, up to 4096 keys, 140 us, of which the copies to LDS alone (four row
 // blocks read each key, 10 TB/s) take 74; 8192 keys of one sequence, 16 heads, 11.5 us and 7.3 for the
 // join, all latency.
 #include "chunk_dr.h"
@@ -387,10 +387,9 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
             float alpha[MT];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                float top = mx[0][16 * mt + r];
+                float now = m[mt];
 #pragma unroll
-                for (int g = 1; g < KG; ++g) top = fmaxf(top, mx[g][16 * mt + r]);
-                const float now = top > m[mt] + LAZY ? top : m[mt];
+                for (int g = 0; g < KG; ++g) now = fmaxf(now, mx[g][16 * mt + r]);
                 alpha[mt] = ex2(m[mt] - (now == -INFINITY ? 0.f : now));
                 same = same && alpha[mt] == 1.f;
                 m[mt] = now;

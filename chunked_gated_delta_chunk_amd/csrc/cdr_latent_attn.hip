@@ -232,9 +232,15 @@ __device__ __forceinline__ void load_keys(const LatentAttnArgs& a, const Seq& s,
 }
 
 // o and lse of a block of 128 rows: two workgroups a CU, so that one's products cover the other's softmax; a
-// wave is preferred during its products, so that the two stay apart.  8192 tokens, 16 heads: 353 us, 0.97
-// PFLOP/s, the matrix unit 58 % busy; the softmax's arithmetic, which both workgroups of a SIMD share, and the
-// waits at its ends bound the rest.  (Cold: rescaling o at every new maximum and without the preference 348 us, lazily 338, with both 334.)
+// wave is preferred during its products, so that the two stay apart.
+//
+// A row's running maximum m is raised by a larger score only where that key's weight is over a sixteenth of the
+// sum so far, or over 2^8: o is otherwise rescaled in most tiles, some row or other having met a slightly larger
+// score.  Weights over 1 are as exact in bf16 and their sums in fp32; but the largest weight is 1 and exact where m
+// is its score, and so it stays for every key that carries a sixteenth of its row or more.
+//
+// 8192 tokens, 16 heads: 353 us, 0.97 PFLOP/s, the matrix unit 58 % busy; the softmax's arithmetic, which both
+// workgroups of a SIMD share, and the waits at its ends bound the rest.
 __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     __shared__ __align__(256) char lds[A_LDS];
     char* kn = lds;
@@ -279,6 +285,8 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
         const char* tn = kn + buf * A_TILE * 256;
         const char* tr = kr + buf * A_TILE * 128;
         const char* tv = vt + buf * A_TILE * 256;
+        // a score over this raises m; worked out here, where the products cover it
+        const float bound = m + fminf(fmaxf(lg2((l + __shfl_xor(l, 32, 64)) * (1.f / 16.f)), 0.f), 8.f);
         f32x16 sc[2] = {zero16(), zero16()};
         bf16x8 f[2][2][2];
         auto read_keys = [&](int batch) {
@@ -316,7 +324,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[t][i]);
         top = fmaxf(top, __shfl_xor(top, 32, 64)) * a.scale2;
-        const float now = top > m + LAZY ? top : m;
+        const float now = top > bound ? top : m;
         const float ref = now == -INFINITY ? 0.f : now;
         const float alpha = ex2(m - ref);
         m = now;
