@@ -239,8 +239,9 @@ __device__ __forceinline__ void load_keys(const LatentAttnArgs& a, const Seq& s,
 // score.  Weights over 1 are as exact in bf16 and their sums in fp32; but the largest weight is 1 and exact where m
 // is its score, and so it stays for every key that carries a sixteenth of its row or more.
 //
-// 8192 tokens, 16 heads: 353 us, 0.97 PFLOP/s, the matrix unit 58 % busy; the softmax's arithmetic, which both
-// workgroups of a SIMD share, and the waits at its ends bound the rest.
+// 8192 tokens, 16 heads: 369 us, 0.93 PFLOP/s, the matrix unit 56 % busy; the softmax's arithmetic, which both
+// workgroups of a SIMD share, and the waits at its ends bound the rest.  (One call alone 352 us; with o rescaled at
+// every new maximum 380, and 373 so without the preference.)
 __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     __shared__ __align__(256) char lds[A_LDS];
     char* kn = lds;
@@ -375,8 +376,8 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
 //
 // Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than two a CU, and a block's own
 // time is what counts (4 packed sequences with gradients, 8192 tokens: 16 heads 666 us with 128 and 615 with 256
-// rows, 8 heads 392 and 417; 1001 tokens of 8 heads 56 and 66).  8192 tokens, 16 heads: 541 us, the matrix unit
-// 55 % busy, 1.02 PFLOP/s with the scores that it computes again.
+// rows, 8 heads 392 and 417; 1001 tokens of 8 heads 56 and 66).  8192 tokens, 16 heads: 573 us, the matrix unit
+// 55 % busy, 0.96 PFLOP/s with the scores that it computes again.
 template <int ROWS>
 __global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kernel(LatentAttnArgs a, const uint16_t* o) {
     constexpr int NW = ROWS / 32;
@@ -517,7 +518,7 @@ __global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kerne
 
 // dk and dv of a block of 128 keys, and the head's part of dkr: one wave a SIMD, whose 512 registers hold v and
 // the 10 blocks of sums; the softmax of one half tile runs between the products of the other.  8192 tokens, 16
-// heads: 767 us, 0.90 PFLOP/s, the matrix unit 47 % busy: with one wave a SIMD, waits for LDS reads are not covered.
+// heads: 810 us, 0.85 PFLOP/s, the matrix unit 47 % busy: with one wave a SIMD, waits for LDS reads are not covered.
 __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
     __shared__ __align__(256) char lds[A_LDS];
     __shared__ __align__(256) char own[A_ROWS * (256 + 128)];   // this block's keys, 32 a wave: operands like v's,

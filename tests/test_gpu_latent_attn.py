@@ -206,6 +206,17 @@ def test_scales_and_large_scores():
     run(kw, do)
 
 
+@pytest.mark.parametrize("rise", [0.5, 2.0, 8.0])
+def test_scores_that_grow_along_the_keys(rise):
+    """The running maximum is met again and again, by a little or by a lot."""
+    kw, do = make([500], [640], 2, 46)
+    kw["q"] = (kw["q"].float() * 0.1 + 1).to(BF16)
+    step = torch.linspace(0, 1, 640).view(1, 640, 1, 1) * rise
+    kw["k_nope"] = (kw["k_nope"].float() * 0.1 + step).to(BF16)
+    kw["k_rope"] = (kw["k_rope"].float() * 0.1 + step[..., 0]).to(BF16)
+    run(kw, do)
+
+
 def test_no_tokens():
     kw, do = make([0], [0], 2, 28, packed=False)
     d = dev(kw)
