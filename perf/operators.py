@@ -30,35 +30,35 @@ BF16, F32 = torch.bfloat16, torch.float32
 def listed():
     return [
         # one decode step's gated head norm: 256 sequences x 16 heads of 128
-        dict(name="gated head norm decode", kind="norm", rows=256 * 16, D=128, post=True, gate="sigmoid",
+        dict(name="gated head norm, decode", kind="norm", rows=256 * 16, D=128, post=True, gate="sigmoid",
              residual=False, pre=False, scale=False, dtype="bf16", res="bf16", train=False),
         # prefill of 8192 tokens at width 2048: norm, gate, learned residual scale, fp32 residual stream, next norm
-        dict(name="block norm 8192 x 2048", kind="norm", rows=8192, D=2048, post=True, gate="silu",
+        dict(name="block norm, 8192 x 2048", kind="norm", rows=8192, D=2048, post=True, gate="silu",
              residual=True, pre=True, scale=True, dtype="bf16", res="fp32", train=False),
         # the same block boundary in a training step
-        dict(name="block norm train 8192 x 2048", kind="norm", rows=8192, D=2048, post=True, gate="silu",
+        dict(name="block norm train, 8192 x 2048", kind="norm", rows=8192, D=2048, post=True, gate="silu",
              residual=True, pre=True, scale=True, dtype="bf16", res="bf16", train=True),
         # an odd width and row count, everything in fp32, residual add and next norm without a gate
-        dict(name="residual norm train odd", kind="norm", rows=1021, D=1537, post=False, gate="none",
+        dict(name="residual norm train, odd", kind="norm", rows=1021, D=1537, post=False, gate="none",
              residual=True, pre=True, scale=True, dtype="fp32", res="fp32", train=True),
         # a decode step of 256 requests, one token each
-        dict(name="page tables decode", kind="pages", n=256, context=8192, new=1, ragged=True, page=64, spare=0),
+        dict(name="page tables, decode", kind="pages", n=256, context=8192, new=1, ragged=True, page=64, spare=0),
         # a ragged prefill of 64 requests, up to 2048 tokens each, padded to a captured size
-        dict(name="page tables prefill", kind="pages", n=64, context=1024, new=2048, ragged=True, page=16,
+        dict(name="page tables, prefill", kind="pages", n=64, context=1024, new=2048, ragged=True, page=16,
              spare=1000),
         # one user, one token: latency
-        dict(name="latent decode 1 x 8192", kind="decode", n=1, t=1, H=16, context=8192, ragged=False, page=64),
+        dict(name="latent decode, 1 x 8192", kind="decode", n=1, t=1, H=16, context=8192, ragged=False, page=64),
         # a full serving batch of ragged lengths, 16 heads a device
-        dict(name="latent decode 256 ragged", kind="decode", n=256, t=1, H=16, context=8192, ragged=True, page=64),
+        dict(name="latent decode, 256 ragged", kind="decode", n=256, t=1, H=16, context=8192, ragged=True, page=64),
         # four draft tokens a sequence, 64 heads
-        dict(name="latent decode 64 x 4 drafts", kind="decode", n=64, t=4, H=64, context=4096, ragged=True, page=16),
+        dict(name="latent decode, 64 x 4 drafts", kind="decode", n=64, t=4, H=64, context=4096, ragged=True, page=16),
         # a packed prefill, odd lengths, 16 heads
-        dict(name="latent attention packed", kind="attn", n=5, T=8168, H=16, context=0, ragged=True, train=False),
+        dict(name="latent attention, packed", kind="attn", n=5, T=8168, H=16, context=0, ragged=True, train=False),
         # one long training sequence, forward and backward
-        dict(name="latent attention train 8192", kind="attn", n=1, T=8192, H=16, context=0, ragged=False,
+        dict(name="latent attention train, 8192", kind="attn", n=1, T=8192, H=16, context=0, ragged=False,
              train=True),
         # a short ragged training batch
-        dict(name="latent attention train ragged", kind="attn", n=7, T=1001, H=8, context=0, ragged=True,
+        dict(name="latent attention train, ragged", kind="attn", n=7, T=1001, H=8, context=0, ragged=True,
              train=True),
     ]
 
