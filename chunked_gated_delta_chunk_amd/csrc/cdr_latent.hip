@@ -64,7 +64,8 @@ struct LatentDecodeArgs {
 };
 
 struct SeqInfo {
-    int bos, tokens, len;    // first new token, new tokens, keys
+    int bos, tokens, len;    // first new token, new tokens, keys that the table has room for
+    int total;               // seq_lens, from which the rows' limits count
 };
 
 __device__ __forceinline__ SeqInfo dec_seq(const LatentDecodeArgs& a, int n) {
@@ -77,7 +78,8 @@ __device__ __forceinline__ SeqInfo dec_seq(const LatentDecodeArgs& a, int n) {
         s.tokens = a.T;
     }
     const int64_t room = (int64_t)a.cols << a.shift;
-    s.len = (int)min((int64_t)max(a.lens[n], 0), min(room, (int64_t)INT32_MAX - 127));   // key numbers of a whole tile stay in int
+    s.total = max(a.lens[n], 0);
+    s.len = (int)min((int64_t)s.total, min(room, (int64_t)INT32_MAX - 127));   // key numbers of a whole tile stay in int
     return s;
 }
 
@@ -288,7 +290,7 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
             int64_t row = (int64_t)rb * M + 16 * (rh * MQ + mt) + r;
             if (row >= rows) row = 0;
             const int tok = (int)(row / a.H), h = (int)(row - (int64_t)tok * a.H);
-            lim[mt] = min(s.len, s.len - s.tokens + tok + 1);
+            lim[mt] = s.total - s.tokens + tok + 1;   // (keys from len on are not there)
             const uint16_t* c = a.qc + (s.bos + tok) * a.qct + h * a.qch;
             const uint16_t* p = a.qr + (s.bos + tok) * a.qrt + h * a.qrh;
 #pragma unroll
@@ -361,7 +363,7 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
                             sc[kt][mt] = mfma32(f[batch & 1][i][kt], qf[mt][STEPS * batch + i], sc[kt][mt]);
                 keep_order();
             }
-            const bool whole = there == ~0ull && 64 * j + 63 <= s.len - s.tokens;
+            const bool whole = there == ~0ull && 64 * j + 63 <= s.total - s.tokens;
 #pragma unroll
             for (int mt = 0; mt < MQ; ++mt) {
                 float t = -INFINITY;

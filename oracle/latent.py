@@ -23,7 +23,8 @@ def decode(q_latent, q_rope, cache, block_table, seq_lens, scale, cu_seqlens=Non
     qc, qr = qc.reshape(B * T, H, 512), qr.reshape(B * T, H, 64)
     cu = [n * T for n in range(B + 1)] if cu_seqlens is None else cu_seqlens.tolist()
     for n in range(len(cu) - 1):
-        length = min(max(lens[n], 0), len(table[n]) * page)
+        total = max(lens[n], 0)
+        length = min(total, len(table[n]) * page)
         keys = torch.zeros(length, 576, dtype=torch.float64)
         there = torch.zeros(length, dtype=torch.bool)
         for j in range(length):
@@ -34,7 +35,7 @@ def decode(q_latent, q_rope, cache, block_table, seq_lens, scale, cu_seqlens=Non
         new = cu[n + 1] - cu[n]
         for i in range(new):
             t = cu[n] + i
-            seen = there & (torch.arange(length) < length - new + i + 1)
+            seen = there & (torch.arange(length) < total - new + i + 1)
             if not seen.any():
                 o[t], mag[t], size[t], lse[t] = 0, 0, 0, -math.inf
                 continue

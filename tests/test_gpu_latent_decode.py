@@ -119,6 +119,20 @@ def test_lengths_beyond_the_table_are_cut():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T", [2, 4, 70])
+@pytest.mark.parametrize("H", [4, 16, 40])
+def test_new_tokens_beyond_the_table(T, H):
+    """New tokens that found no room in the table: those before them see what they would see in a longer
+    table whose further pages are not there."""
+    kw = make([63, 40, 0, 64], T, H, 16, 10 * T + H, spare_cols=0)
+    kw["seq_lens"] = torch.tensor([63 + T, 40 + T, T, 64 + T], dtype=torch.int32)
+    kw["cache"][torch.isnan(kw["cache"])] = 0.5      # the tail of a last page is a new token's now
+    wider = dict(kw, block_table=torch.cat([kw["block_table"], torch.full((4, 5), -1, dtype=torch.int32)], 1))
+    o, lse = cdr.latent_decode_fwd(**dev(kw), scale=SCALE)
+    compare(wider, o, lse)
+    compare(kw, o, lse)
+
+
 @pytest.mark.parametrize("H", [5, 16, 40])
 def test_packed_queries(H):
     packed = [1, 4, 0, 2, 9]
