@@ -44,6 +44,8 @@ namespace {
 constexpr int DEC_GRID = 256;        // workgroups; LDS holds one on a CU
 constexpr int DEC_KEYS = 64;         // keys of a tile
 constexpr int DEC_TEAM = 8;          // most row blocks that are taken side by side
+// Keys of a sequence at most: pages are looked up two tiles ahead, up to key len + 190, which stays in int.
+constexpr int64_t DEC_MAX_LEN = (int64_t)INT32_MAX - 255;
 
 struct LatentDecodeArgs {
     const uint16_t* qc;
@@ -79,7 +81,7 @@ __device__ __forceinline__ SeqInfo dec_seq(const LatentDecodeArgs& a, int n) {
     }
     const int64_t room = (int64_t)a.cols << a.shift;
     s.total = max(a.lens[n], 0);
-    s.len = (int)min((int64_t)s.total, min(room, (int64_t)INT32_MAX - 127));   // key numbers of a whole tile stay in int
+    s.len = (int)min((int64_t)s.total, min(room, DEC_MAX_LEN));
     return s;
 }
 

@@ -539,8 +539,8 @@ cdr_status cdr_build_page_tables(int32_t N, int32_t table_cols, int32_t num_free
  *
  * so seq_lens counts the new tokens, whose keys are written first (cdr_latent_cache_write).  Key j
  * of sequence n is row block_table[n, j / page_size] * page_size + j % page_size of the cache.
- * Keys beyond table_cols * page_size and keys whose page lies outside [0, num_pages) do not exist:
- * they are masked and not read; seq_lens may count them, and the rows' limits count from it all the
+ * Keys beyond table_cols * page_size or 2^31 - 256 and keys whose page lies outside [0, num_pages) do not
+ * exist: they are masked and not read; seq_lens may count them, and the rows' limits count from it all the
  * same.  A row left without keys gives o = 0 and lse = -inf.  What lies behind a sequence's last key,
  * in its last page or elsewhere, does not affect it, whatever it holds; keys below seq_lens[n] must be
  * finite, those that a row's causal limit hides from it too (they meet a weight of zero).

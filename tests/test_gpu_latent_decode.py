@@ -133,6 +133,32 @@ def test_new_tokens_beyond_the_table(T, H):
     compare(kw, o, lse)
 
 
+def test_the_most_keys_a_sequence_can_have():
+    """A length of 2^31 - 1 over a table with room for as many: only its first and last page are there, the last
+    up to key 2^31 - 256, and both are one page of the cache."""
+    page, cols = 2 ** 16, 2 ** 15
+    g = torch.Generator().manual_seed(20)
+    q = torch.randn(1, 1, 3, 576, generator=g).to(BF16)
+    cache = torch.randn(1, page, 576, generator=g).to(BF16)
+    table = torch.full((1, cols), -1, dtype=torch.int32)
+    table[0, 0] = table[0, -1] = 0
+    o, lse = cdr.latent_decode_fwd(q[..., :512].to(DEV), q[..., 512:].to(DEV), cache.to(DEV), table.to(DEV),
+                                   torch.tensor([2 ** 31 - 1], dtype=torch.int32, device=DEV), SCALE)
+    keys = cache[0].double()
+    twice = torch.full((page,), math.log(2.0), dtype=torch.float64)
+    twice[-256:] = 0
+    s = SCALE * (q[0, 0].double() @ keys.T) + twice
+    p = torch.softmax(s, -1)
+    size = SCALE * (q[0, 0].double().abs() @ keys.abs().T).amax(-1)
+    # as in compare(), the sums taken over the 1024 tiles of a page one after the other, two roundings each
+    e = 585 * 2.0 ** -24 * size + (80 + 2 * 1024) * 2.0 ** -24
+    lse_ref = torch.logsumexp(s, -1)
+    assert ((lse[0, 0].cpu().double() - lse_ref).abs() <= e + 2.0 ** -22 * lse_ref.abs()).all()
+    ref, mag = p @ keys[:, :512], p @ keys[:, :512].abs()
+    tol = (2.0 ** -8 + 2 * e + 2.0 ** -16)[:, None] * mag + 2.0 ** -8 * ref.abs()
+    assert ((o[0, 0].cpu().double() - ref).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("H", [5, 16, 40])
 def test_packed_queries(H):
     packed = [1, 4, 0, 2, 9]
