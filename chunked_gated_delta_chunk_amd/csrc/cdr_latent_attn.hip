@@ -767,8 +767,8 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
 __global__ __launch_bounds__(256) void latent_dkr_kernel(const float* part, uint16_t* dkr, const int32_t* cuk, int N, int total,
                                                          int H) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t keys = cuk ? min(max(cuk[N], 0), total) : total;
-    if (i >= keys * (LR / 4)) return;
+    const int64_t first = cuk ? min(max(cuk[0], 0), total) : 0, end = cuk ? min(max(cuk[N], 0), total) : total;
+    if (i < first * (LR / 4) || i >= end * (LR / 4)) return;   // only held keys have parts
     f32x4 t = {0.f, 0.f, 0.f, 0.f};
     for (int h = 0; h < H; ++h) t += *reinterpret_cast<const f32x4*>(part + ((size_t)h * total) * LR + 4 * i);
     *reinterpret_cast<uint2*>(dkr + 4 * i) = make_uint2(pack_bf2(t[0], t[1]), pack_bf2(t[2], t[3]));

@@ -654,8 +654,8 @@ cdr_status cdr_latent_attn_fwd(const cdr_latent_attn_problem* p, const void* q, 
  *
  *   o, lse    as the forward wrote them;  d_o bf16 [tokens, H, 128] dense
  *   dq        bf16 [tokens, H, 192], dk_nope bf16 [keys, H, 128], dk_rope bf16 [keys, 64] (the sum
- *             over the heads, added in fp32), dv bf16 [keys, H, 128]; dense.  Rows and keys behind the
- *             last sequence are left as they were.
+ *             over the heads, added in fp32), dv bf16 [keys, H, 128]; dense.  Rows and keys that no
+ *             sequence holds (in front of the first offset, behind the last) are left as they were.
  *   workspace at least cdr_latent_attn_bwd_workspace_bytes(p) bytes, 16-byte aligned, contents
  *             irrelevant, not to be used by another call until this one's kernels have finished
  * No output may overlap an input.  No atomics: repeated calls give the same bits.

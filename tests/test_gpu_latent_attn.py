@@ -11,12 +11,14 @@ output's last product:
             as the forward rounded it, (2^-8 + 2^-8 + 2 e + 2^-16) of its absolute terms; dS is rounded
             to bf16: 2^-8; together (4 2^-8 + 4 e + 2^-14) mag + half a step
 """
+import ctypes
 import math
 
 import pytest
 import torch
 
 import chunked_gated_delta_chunk_amd as cdr
+from chunked_gated_delta_chunk_amd import latent
 from oracle import latent as oracle_latent
 
 pytestmark = pytest.mark.gpu
@@ -124,6 +126,44 @@ def test_behind_the_last_sequence_is_left_alone():
     out[:, 71:], lse[:, 71:] = math.nan, math.nan
     grads = cdr.latent_attn_bwd(**d, o=out, lse=lse, do=do.to(DEV))
     compare(kw, do, out, lse, grads, 192 ** -0.5)
+
+
+def raw_bwd(kw, do, o, lse, varlen, fill=3.0):
+    """cdr_latent_attn_bwd itself, over outputs and a workspace that hold `fill`."""
+    c = latent._LatentAttn(kw["q"], kw["k_nope"], kw["k_rope"], kw["v"], None, kw["cu_seqlens"], kw["cu_seqlens_k"], "")
+    c.p.varlen = varlen
+    full = lambda *s: torch.full(s, fill, dtype=BF16, device=DEV)  # noqa: E731
+    dq, dk, dv = full(1, c.T, c.H, 192), full(1, c.Tk, c.H, 128), full(1, c.Tk, c.H, 128)
+    dkr = full(1, c.Tk, 64)
+    need = c.lib.cdr_latent_attn_bwd_workspace_bytes(ctypes.byref(c.p))
+    work = torch.full((need // 4,), fill, device=DEV)
+    st = c.lib.cdr_latent_attn_bwd(ctypes.byref(c.p), *c.inputs, o.data_ptr(), lse.data_ptr(), do.data_ptr(),
+                                   dq.data_ptr(), dk.data_ptr(), dkr.data_ptr(), dv.data_ptr(), work.data_ptr(), need,
+                                   torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    return dq, dk, dkr, dv
+
+
+def gaps(seed):
+    """Two sequences with rows and keys in front of the first (7 and 9) and behind the last (5 each), NaN and infinite."""
+    kw, do = make([7, 30, 41], [9, 50, 41], 2, seed, spare=5)
+    kw["cu_seqlens"], kw["cu_seqlens_k"] = kw["cu_seqlens"][1:], kw["cu_seqlens_k"][1:]
+    d, ddo = dev(kw), do.to(DEV)
+    for name in ("q", "k_nope", "k_rope", "v"):
+        a, b = (7, 78) if name == "q" else (9, 100)
+        d[name][:, :a], d[name][:, b:] = math.nan, math.inf
+    ddo[:, :7], ddo[:, 78:] = math.nan, math.nan
+    return kw, do, d, ddo
+
+
+def test_gradients_that_no_sequence_holds_are_left_alone():
+    kw, do, d, ddo = gaps(60)
+    o, lse = cdr.latent_attn_fwd(**d)
+    grads = raw_bwd(d, ddo, o, lse, 1)
+    compare(kw, do, o, lse, grads, 192 ** -0.5)
+    for name, g in zip(NAMES, grads):
+        a, b = (7, 78) if name == "dq" else (9, 100)
+        assert (g[:, :a] == 3).all() and (g[:, b:] == 3).all(), name
 
 
 def test_neighbours_of_a_sequence_do_not_matter():
