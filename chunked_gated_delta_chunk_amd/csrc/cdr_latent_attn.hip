@@ -56,6 +56,7 @@ struct LatentAttnArgs {
     int64_t qt, qh, kt, kh, rt, vt, vh;   // strides, elements
     int T, Tk, H, N, slots, total_k;
     int ranked;         // blocks by weight rather than by slot
+    int fill;           // rows (keys) that no sequence holds are written too
     float scale, scale2;
 };
 
@@ -382,6 +383,8 @@ template <int ROWS>
 __global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kernel(LatentAttnArgs a, const uint16_t* o) {
     constexpr int NW = ROWS / 32;
     __shared__ __align__(256) char lds[A_LDS + ROWS * 256];
+    if (a.fill)
+        fill_unheld(reinterpret_cast<uint4*>(a.o), a.H * (AQ / 8), make_uint4(0, 0, 0, 0), a.cuq, a.N, a.T, blockIdx.x, gridDim.x);
     const int h = blockIdx.x % a.H;
     int n, block;
     if (!attn_block<ROWS, false>(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;
@@ -528,6 +531,11 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
     char* qr = qn + 2 * A_TILE * 256;
     char* td = qr + 2 * A_TILE * 128;
     const uint32_t qn0 = lds_offset(qn), qr0 = lds_offset(qr), td0 = lds_offset(td);
+    if (a.fill) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        fill_unheld(reinterpret_cast<uint4*>(a.dk), a.H * (AN / 8), zero, a.cuk, a.N, a.Tk, blockIdx.x, gridDim.x);
+        fill_unheld(reinterpret_cast<uint4*>(a.dv), a.H * (AV / 8), zero, a.cuk, a.N, a.Tk, blockIdx.x, gridDim.x);
+    }
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = blockIdx.x % a.H;
     int n, block;
@@ -765,12 +773,13 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
 // dkr: the heads' parts added in order, 4 dimensions a thread.  8192 tokens, 16 heads: 7.5 us, 34 MB, mostly from
 // the Infinity Cache.
 __global__ __launch_bounds__(256) void latent_dkr_kernel(const float* part, uint16_t* dkr, const int32_t* cuk, int N, int total,
-                                                         int H) {
+                                                         int H, int fill) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t first = cuk ? min(max(cuk[0], 0), total) : 0, end = cuk ? min(max(cuk[N], 0), total) : total;
-    if (i < first * (LR / 4) || i >= end * (LR / 4)) return;   // only held keys have parts
+    const bool held = i >= first * (LR / 4) && i < end * (LR / 4);   // only such keys have parts
+    if (!held && (!fill || i >= (int64_t)total * (LR / 4))) return;
     f32x4 t = {0.f, 0.f, 0.f, 0.f};
-    for (int h = 0; h < H; ++h) t += *reinterpret_cast<const f32x4*>(part + ((size_t)h * total) * LR + 4 * i);
+    for (int h = 0; h < (held ? H : 0); ++h) t += *reinterpret_cast<const f32x4*>(part + ((size_t)h * total) * LR + 4 * i);
     *reinterpret_cast<uint2*>(dkr + 4 * i) = make_uint2(pack_bf2(t[0], t[1]), pack_bf2(t[2], t[3]));
 }
 
@@ -807,6 +816,7 @@ LatentAttnArgs attn_args(const cdr_latent_attn_problem* p, const void* q, const 
     a.vt = p->v_stride[0], a.vh = p->v_stride[1];
     a.T = p->T, a.Tk = p->Tk, a.H = p->H, a.N = p->N;
     a.total_k = (int)total_k(p);
+    a.fill = p->varlen == CDR_VARLEN_FILL;
     a.scale = p->scale;
     a.scale2 = p->scale * LOG2E;
     return a;
@@ -897,7 +907,7 @@ cdr_status cdr_latent_attn_bwd(const cdr_latent_attn_problem* p, const void* q, 
         hipLaunchKernelGGL(cdr::latent_dkv_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a);
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
         hipLaunchKernelGGL(cdr::latent_dkr_kernel, dim3((unsigned)((tk * (cdr::LR / 4) + 255) / 256)), dim3(256), 0, s, a.dkr,
-                           static_cast<uint16_t*>(dk_rope), a.cuk, p->N, (int)tk, p->H);
+                           static_cast<uint16_t*>(dk_rope), a.cuk, p->N, (int)tk, p->H, a.fill);
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
     }
     return CDR_OK;

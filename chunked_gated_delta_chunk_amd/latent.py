@@ -13,6 +13,7 @@ from .blocks import _launch, _need_gpu, _on, _ptr
 from .ops import CDR_OK, _need, _raise, load_library
 
 LATENT_DIM, LATENT_ROPE = 512, 64
+VARLEN_FILL = 2   # CDR_VARLEN_FILL of chunk_dr.h
 
 
 _STRIDE_LIMIT = 1 << 23   # elements: the kernels step over a tile's rows in 32 bits
@@ -269,8 +270,8 @@ def latent_attn_bwd(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor,
 
     Inputs as the forward, its ``o`` and ``lse``, and ``do [B,T,H,128]`` bf16, the gradient of o.
     Returns bf16 ``(dq, dk_nope, dk_rope, dv)`` with the shapes of the inputs; dk_rope is the sum
-    over the heads, added in fp32.  Repeated calls give the same bits.  ``workspace`` optionally
-    supplies the scratch buffer (uint8, contiguous).
+    over the heads, added in fp32.  Rows and keys that no packed sequence holds get zeros.  Repeated
+    calls give the same bits.  ``workspace`` optionally supplies the scratch buffer (uint8, contiguous).
     """
     c = _LatentAttn(q, k_nope, k_rope, v, scale, cu_seqlens, cu_seqlens_k, "latent_attn_bwd")
     shape = (c.B, c.T, c.H, VALUE_DIM)
@@ -291,6 +292,8 @@ def latent_attn_bwd(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor,
     dq = empty(c.B, c.T, c.H, QUERY_DIM)
     dk, dv = empty(c.B, c.Tk, c.H, NOPE_DIM), empty(c.B, c.Tk, c.H, VALUE_DIM)
     dkr = empty(c.B, c.Tk, LATENT_ROPE)
+    if c.p.varlen:
+        c.p.varlen = VARLEN_FILL
     _launch(c.device, "latent_attn_bwd", c.lib.cdr_latent_attn_bwd, ctypes.byref(c.p), *c.inputs, _ptr(o), _ptr(lse),
             _ptr(do), _ptr(dq), _ptr(dk), _ptr(dkr), _ptr(dv), _ptr(workspace),
             workspace.numel() * workspace.element_size())

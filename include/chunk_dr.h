@@ -559,6 +559,8 @@ cdr_status cdr_build_page_tables(int32_t N, int32_t table_cols, int32_t num_free
  * enter the second product as bf16 (the first product's sum of them does not).  Lengths are read on
  * the device, so a captured call serves any lengths.  Repeated calls give the same bits.
  * ------------------------------------------------------------------------------------------ */
+#define CDR_VARLEN_FILL 2      /* varlen of latent attention's gradients: packed, and rows and keys that no
+                                  sequence holds are written too */
 #define CDR_LATENT_DIM 512
 #define CDR_LATENT_ROPE 64
 
@@ -655,7 +657,8 @@ cdr_status cdr_latent_attn_fwd(const cdr_latent_attn_problem* p, const void* q, 
  *   o, lse    as the forward wrote them;  d_o bf16 [tokens, H, 128] dense
  *   dq        bf16 [tokens, H, 192], dk_nope bf16 [keys, H, 128], dk_rope bf16 [keys, 64] (the sum
  *             over the heads, added in fp32), dv bf16 [keys, H, 128]; dense.  Rows and keys that no
- *             sequence holds (in front of the first offset, behind the last) are left as they were.
+ *             sequence holds (in front of the first offset, behind the last) are left as they were,
+ *             or set to zero with varlen CDR_VARLEN_FILL.
  *   workspace at least cdr_latent_attn_bwd_workspace_bytes(p) bytes, 16-byte aligned, contents
  *             irrelevant, not to be used by another call until this one's kernels have finished
  * No output may overlap an input.  No atomics: repeated calls give the same bits.

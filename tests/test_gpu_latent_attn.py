@@ -166,6 +166,33 @@ def test_gradients_that_no_sequence_holds_are_left_alone():
         assert (g[:, :a] == 3).all() and (g[:, b:] == 3).all(), name
 
 
+def test_gradients_that_no_sequence_holds_are_zero(monkeypatch):
+    """From the C entry over what the outputs held before, and from the binding, whatever memory it gets."""
+    kw, do, d, ddo = gaps(61)
+    o, lse = cdr.latent_attn_fwd(**d)
+    filled = raw_bwd(d, ddo, o, lse, latent.VARLEN_FILL, fill=math.nan)
+    empty = torch.empty
+    with monkeypatch.context() as m:
+        m.setattr(torch, "empty", lambda *s, **k: empty(*s, **k).fill_(77))
+        grads = cdr.latent_attn_bwd(**d, o=o, lse=lse, do=ddo)
+    compare(kw, do, o, lse, grads, 192 ** -0.5)
+    for name, g, f in zip(NAMES, grads, filled):
+        a, b = (7, 78) if name == "dq" else (9, 100)
+        assert (g[:, :a] == 0).all() and (g[:, b:] == 0).all(), name
+        assert torch.equal(g, f), name
+
+
+def test_gradients_of_padding_alone_and_of_many_rows_of_it():
+    """No sequence with a token, and a tail far longer than the launch has workgroups."""
+    for lens, spare in (((0, 0), 300), ((3,), 9000)):
+        kw, do = make(lens, lens, 1, 62, spare=spare)
+        d = dev(kw)
+        o, lse = cdr.latent_attn_fwd(**d)
+        grads = cdr.latent_attn_bwd(**d, o=o, lse=lse, do=do.to(DEV))
+        compare(kw, do, o, lse, grads, 192 ** -0.5)
+        assert all((g[:, sum(lens):] == 0).all() for g in grads)
+
+
 def test_neighbours_of_a_sequence_do_not_matter():
     """The same sequence between others that hold NaN, with the same bits."""
     kw, do = make([77], [90], 2, 24)
