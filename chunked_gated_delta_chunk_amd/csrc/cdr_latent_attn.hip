@@ -249,6 +249,10 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     char* kr = kn + 2 * A_TILE * 256;
     char* vt = kr + 2 * A_TILE * 128;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (a.fill) {
+        fill_unheld(reinterpret_cast<uint4*>(a.o), a.H * (AV / 8), make_uint4(0, 0, 0, 0), a.cuq, a.N, a.T, blockIdx.x, gridDim.x);
+        fill_unheld(a.lse, a.H, -INFINITY, a.cuq, a.N, a.T, blockIdx.x, gridDim.x);
+    }
     const int h = blockIdx.x % a.H;
     int n, block;
     if (!attn_block<A_ROWS, false>(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;

@@ -4,6 +4,7 @@ paged cache, for decoding, and the expanded form with its gradients, for prefill
 Argument marshalling only, as in ops.py.
 """
 import ctypes
+import math
 from typing import Optional, Tuple
 
 import torch
@@ -48,6 +49,24 @@ def _tokens(t):
     if t.stride(0) != T * t.stride(1):
         t = t.contiguous()
     return t, t.stride(1)
+
+
+def _results(p, out, lse_out, shape, device):
+    """The outputs of a forward.  What packed sequences do not hold becomes zeros and -inf in those made here,
+    written by the kernels (VARLEN_FILL) where both are."""
+    if p.varlen and (out is None) != (lse_out is None):
+        if out is None:
+            out = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+        else:
+            lse_out = torch.full(shape[:3], -math.inf, dtype=torch.float32, device=device)
+    elif out is None or lse_out is None:
+        if p.varlen:
+            p.varlen = VARLEN_FILL
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        if lse_out is None:
+            lse_out = torch.empty(shape[:3], dtype=torch.float32, device=device)
+    return out, lse_out
 
 
 def latent_cache_write(c: torch.Tensor, k_rope: torch.Tensor, cache: torch.Tensor, slot_map: torch.Tensor) -> None:
@@ -240,9 +259,9 @@ def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor,
     query sees all Tk keys, so ``Tk - T`` earlier keys are a context; a query without keys gives
     zeros and -inf.  Packed batches have B = 1, ``cu_seqlens`` int32 ``[N+1]`` for the queries and
     ``cu_seqlens_k`` for the keys (the same when None).  ``scale=None`` means ``192 ** -0.5``; it must
-    be positive.  Returns ``(o, lse)``: ``[B,T,H,128]`` bf16 and ``[B,T,H]`` fp32.  ``out`` and
-    ``lse_out`` optionally supply the buffers; rows behind the last packed sequence are left as they
-    were in them.
+    be positive.  Returns ``(o, lse)``: ``[B,T,H,128]`` bf16 and ``[B,T,H]`` fp32; rows that no packed
+    sequence holds are zeros and -inf.  ``out`` and ``lse_out`` optionally supply the buffers; in them
+    such rows are left as they were.
     """
     c = _LatentAttn(q, k_nope, k_rope, v, scale, cu_seqlens, cu_seqlens_k, "latent_attn_fwd")
     if out is not None:
@@ -253,10 +272,7 @@ def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor,
         _need(lse_out, "lse_out", torch.float32, (c.B, c.T, c.H), dense=True)
     _on(c.device, out=out, lse_out=lse_out)
     _need_gpu(c.device)
-    if out is None:
-        out = torch.empty((c.B, c.T, c.H, VALUE_DIM), dtype=torch.bfloat16, device=c.device)
-    if lse_out is None:
-        lse_out = torch.empty((c.B, c.T, c.H), dtype=torch.float32, device=c.device)
+    out, lse_out = _results(c.p, out, lse_out, (c.B, c.T, c.H, VALUE_DIM), c.device)
     _launch(c.device, "latent_attn_fwd", c.lib.cdr_latent_attn_fwd, ctypes.byref(c.p), *c.inputs, _ptr(out),
             _ptr(lse_out))
     return out, lse_out

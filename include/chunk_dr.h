@@ -559,8 +559,8 @@ cdr_status cdr_build_page_tables(int32_t N, int32_t table_cols, int32_t num_free
  * enter the second product as bf16 (the first product's sum of them does not).  Lengths are read on
  * the device, so a captured call serves any lengths.  Repeated calls give the same bits.
  * ------------------------------------------------------------------------------------------ */
-#define CDR_VARLEN_FILL 2      /* varlen of latent attention's gradients: packed, and rows and keys that no
-                                  sequence holds are written too */
+#define CDR_VARLEN_FILL 2      /* varlen of cdr_latent_attn_*: packed, and rows and keys that no sequence
+                                  holds are written too */
 #define CDR_LATENT_DIM 512
 #define CDR_LATENT_ROPE 64
 
@@ -618,8 +618,9 @@ cdr_status cdr_latent_cache_write(int32_t T, int32_t num_pages, int32_t page_siz
  *   v        bf16 [keys, H, 128]                             strides (token, head)
  *   cu_seqlens, cu_seqlens_k  int32 [N + 1], varlen: rows' and keys' offsets, clipped to [0, T] and
  *            [0, Tk]; may be the same array.  Else every sequence has T rows and Tk keys.
- *   o        bf16 [tokens, H, 128], lse fp32 [tokens, H]; dense.  Rows behind the last sequence are
- *            left as they were.
+ *   o        bf16 [tokens, H, 128], lse fp32 [tokens, H]; dense.  Rows that no sequence holds (in front
+ *            of the first offset, behind the last) are left as they were, or become 0 and -inf with
+ *            varlen CDR_VARLEN_FILL.
  * Strides are in elements, multiples of 8, not negative and below 2^23, so k_nope and v may be the
  * two halves of one projection [keys, H, 256]; all but lse are 16-byte aligned.  scale is positive.
  * Values of a sequence must be finite, also those that the causal limit hides from a row (they meet

@@ -156,6 +156,23 @@ def gaps(seed):
     return kw, do, d, ddo
 
 
+def test_results_that_no_sequence_holds_are_empty_rows(monkeypatch):
+    """Zeros and -inf in what the binding allocates, whatever memory it gets; supplied buffers keep theirs."""
+    kw, do, d, _ = gaps(59)
+    empty = torch.empty
+    with monkeypatch.context() as m:
+        m.setattr(torch, "empty", lambda *s, **k: empty(*s, **k).fill_(77))
+        o, lse = cdr.latent_attn_fwd(**d)
+        out, lse_out = torch.full_like(o, 3), torch.full_like(lse, 3)
+        only_lse = cdr.latent_attn_fwd(**d, out=out)[1]
+        only_o = cdr.latent_attn_fwd(**d, lse_out=lse_out)[0]
+    compare(kw, do, o, lse, None, 192 ** -0.5)
+    for x, y, z, value in ((o, only_o, out, 0), (lse, only_lse, lse_out, -math.inf)):
+        for rows in (slice(0, 7), slice(78, 83)):
+            assert (x[:, rows] == value).all() and (z[:, rows] == 3).all()
+        assert torch.equal(x, y) and torch.equal(x[:, 7:78], z[:, 7:78])
+
+
 def test_gradients_that_no_sequence_holds_are_left_alone():
     kw, do, d, ddo = gaps(60)
     o, lse = cdr.latent_attn_fwd(**d)
