@@ -61,6 +61,7 @@ struct LatentDecodeArgs {
     int4* rec;         // [grid] (n, row block, parts) of the unit cut at this workgroup's end
     int64_t qct, qch, qrt, qrh;
     int N, T, H, cols, num_pages, shift;
+    int fill;          // rows that no sequence holds are written too
     int team;          // workgroups that take the row blocks of one sequence side by side
     float scale2;      // scale * log2(e)
 };
@@ -260,6 +261,10 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
     const int r = lane & 15, q = lane >> 4;
     const int kg = w % KG, rh = w / KG;        // the wave's keys and row part in the scores
     const int wg = dec_wg();
+    if (a.fill) {
+        fill_unheld(reinterpret_cast<uint4*>(a.o), a.H * (LC / 8), make_uint4(0, 0, 0, 0), a.cu, a.N, a.T, wg, DEC_GRID);
+        if (a.lse) fill_unheld(a.lse, a.H, -INFINITY, a.cu, a.N, a.T, wg, DEC_GRID);
+    }
     Run run;
     if (!dec_run<M, 64 * NW>(a, wg, run)) return;
     int64_t pos = run.begin;
@@ -680,6 +685,7 @@ cdr_status cdr_latent_decode_fwd(const cdr_latent_decode_problem* p, const void*
     a.qct = p->qc_stride[0], a.qch = p->qc_stride[1];
     a.qrt = p->qr_stride[0], a.qrh = p->qr_stride[1];
     a.N = p->N, a.T = p->T, a.H = p->H;
+    a.fill = p->varlen == CDR_VARLEN_FILL;
     a.cols = p->table_cols;
     a.num_pages = p->num_pages;
     a.shift = __builtin_ctz((unsigned)p->page_size);

@@ -128,9 +128,10 @@ def latent_decode_fwd(q_latent: torch.Tensor, q_rope: torch.Tensor, cache: torch
     has no default: it belongs to the width of the heads before absorption.
 
     Returns ``(o, lse)``: o ``[.., H, 512]`` bf16 (the weighted latents, before the value
-    up-projection) and the log of the sum of exponentials ``[.., H]`` fp32.  ``out``, ``lse_out``
-    and ``workspace`` (uint8, :func:`latent_decode_workspace_bytes`) optionally supply the buffers;
-    rows behind the last packed sequence are left as they were in them.
+    up-projection) and the log of the sum of exponentials ``[.., H]`` fp32; rows that no packed
+    sequence holds are zeros and -inf.  ``out``, ``lse_out`` and ``workspace`` (uint8,
+    :func:`latent_decode_workspace_bytes`) optionally supply the buffers; in the former two such rows
+    are left as they were.
     """
     lib = load_library()
     if not isinstance(q_latent, torch.Tensor) or q_latent.dim() != 4 or q_latent.shape[3] != LATENT_DIM:
@@ -178,10 +179,7 @@ def latent_decode_fwd(q_latent: torch.Tensor, q_rope: torch.Tensor, cache: torch
         raise ValueError("workspace too small")
     elif not workspace.is_contiguous() or workspace.data_ptr() % 16:
         raise ValueError("workspace must be contiguous and 16-byte aligned")
-    if out is None:
-        out = torch.empty((B, T, H, LATENT_DIM), dtype=torch.bfloat16, device=device)
-    if lse_out is None:
-        lse_out = torch.empty((B, T, H), dtype=torch.float32, device=device)
+    out, lse_out = _results(p, out, lse_out, (B, T, H, LATENT_DIM), device)
     block_table, seq_lens = block_table.contiguous(), seq_lens.contiguous()
     cu = None if cu_seqlens is None else cu_seqlens.contiguous()
     _launch(device, "latent_decode_fwd", lib.cdr_latent_decode_fwd, ref, _ptr(qc), _ptr(qr), _ptr(cache),

@@ -550,8 +550,9 @@ cdr_status cdr_build_page_tables(int32_t N, int32_t table_cols, int32_t num_free
  *   cache      bf16 [num_pages, page_size, 576], page_size a power of two
  *   block_table int32 [N, table_cols], seq_lens int32 [N], cu_seqlens int32 [N + 1] (varlen;
  *              offsets are clipped to [0, T])
- *   o          bf16 [tokens, H, 512], lse fp32 [tokens, H] or NULL; rows behind the last sequence
- *              are left as they were
+ *   o          bf16 [tokens, H, 512], lse fp32 [tokens, H] or NULL; rows that no sequence holds (in
+ *              front of the first offset, behind the last) are left as they were, or become 0 and
+ *              -inf with varlen CDR_VARLEN_FILL
  *   workspace  at least cdr_latent_decode_workspace_bytes(p) bytes, 16-byte aligned, contents
  *              irrelevant, not to be used by another call until this one's kernels have finished
  * q, cache, o and the workspace are 16-byte aligned; no output may overlap an input.  Scores and
@@ -559,7 +560,7 @@ cdr_status cdr_build_page_tables(int32_t N, int32_t table_cols, int32_t num_free
  * enter the second product as bf16 (the first product's sum of them does not).  Lengths are read on
  * the device, so a captured call serves any lengths.  Repeated calls give the same bits.
  * ------------------------------------------------------------------------------------------ */
-#define CDR_VARLEN_FILL 2      /* varlen of cdr_latent_attn_*: packed, and rows and keys that no sequence
+#define CDR_VARLEN_FILL 2      /* varlen of latent attention: packed, and rows and keys that no sequence
                                   holds are written too */
 #define CDR_LATENT_DIM 512
 #define CDR_LATENT_ROPE 64

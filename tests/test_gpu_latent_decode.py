@@ -172,6 +172,29 @@ def test_packed_queries(H):
     assert (out[0, total:] == 7).all() and (lse[0, total:] == 7).all()    # behind the last sequence
 
 
+@pytest.mark.parametrize("H,spare", [(5, 2), (40, 600)])
+def test_rows_that_no_sequence_holds_are_empty(H, spare, monkeypatch):
+    """Zeros and -inf in what the binding allocates, whatever memory it gets; supplied buffers keep theirs."""
+    packed = [3, 1, 4, 0, 2]
+    kw = make([9, 30, 64, 50, 129], 0, H, 16, H, packed=packed)
+    wide = lambda t: torch.cat([t, torch.full((1, spare - 2) + t.shape[2:], math.nan, dtype=BF16)], 1)  # noqa: E731
+    kw["q_latent"], kw["q_rope"] = wide(kw["q_latent"]), wide(kw["q_rope"])
+    for n in ("seq_lens", "block_table", "cu_seqlens"):
+        kw[n] = kw[n][1:]                      # the first three rows are nobody's
+    empty, d = torch.empty, dev(kw)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "empty", lambda *s, **k: empty(*s, **k).fill_(77))
+        o, lse = cdr.latent_decode_fwd(**d, scale=SCALE)
+        out, lse_out = torch.full_like(o, 3), torch.full_like(lse, 3)
+        only_lse = cdr.latent_decode_fwd(**d, scale=SCALE, out=out)[1]
+        only_o = cdr.latent_decode_fwd(**d, scale=SCALE, lse_out=lse_out)[0]
+    compare(kw, o, lse)
+    for x, y, z, value in ((o, only_o, out, 0), (lse, only_lse, lse_out, -math.inf)):
+        for rows in (slice(0, 3), slice(10, 10 + spare)):
+            assert (x[:, rows] == value).all() and (z[:, rows] == 3).all()
+        assert torch.equal(x, y) and torch.equal(x[:, 3:10], z[:, 3:10])
+
+
 def test_strided_queries_and_other_scales():
     kw = make([33, 100], 2, 8, 16, 12)
     g = dev(kw)
