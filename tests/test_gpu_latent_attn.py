@@ -276,6 +276,24 @@ def test_dq_in_blocks_of_either_size():
     run(kw, do)
 
 
+@pytest.mark.parametrize("short", [53, 54, 58, 70])
+def test_dq_of_long_sequences_on_both_sides_of_the_larger_blocks(short):
+    """dq takes blocks of 256 rows from 512 of them on (T // 256 + N a head): with 53 short sequences beside three
+    long ones 504 for 8 heads, with 54 just 512; with 70 the blocks go by slot, not by weight."""
+    lq = [1100, 257, 513] + [3] * short
+    run(*make(lq, [1100, 257, 600] + [3, 4, 2, 150, 0, 3, 3] * (short // 7) + [3] * (short % 7), 8, 47 + short))
+
+
+def test_dq_in_the_larger_blocks_of_one_long_sequence():
+    """2500 rows among 55 of one, 520 blocks of 256 for 8 heads."""
+    run(*make([2500] + [1] * 55, [3001] + [1] * 55, 8, 49))
+
+
+def test_dq_in_the_larger_blocks_of_equal_lengths():
+    """11 sequences of 520 rows and 16 heads, 528 blocks: two full ones and a cut one, behind a context."""
+    run(*make([520] * 11, [560] * 11, 16, 48, packed=False))
+
+
 @pytest.mark.parametrize("H", [2, 80])
 def test_rows_on_both_sides_of_128_keys(H):
     """Blocks of either size in which delta comes from the weights for some rows and from o for others, among
