@@ -35,13 +35,22 @@ def _launch(device, what, entry, *args):
         _raise(st, what)
 
 
+def _span(t):
+    """First byte and end of the memory between a tensor's first and last element."""
+    a = t.data_ptr()
+    last = -1 if t.numel() == 0 else sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return a, a + (last + 1) * t.element_size()
+
+
 def _apart(inputs, outputs):
-    """Raises where an output's memory overlaps an input's (both dicts of dense tensors)."""
+    """Raises where an output's memory overlaps that of an input read in place (both dicts, None for none)."""
+    spans = [(m, *_span(i)) for m, i in inputs.items() if i is not None]
     for n, o in outputs.items():
-        a, size = o.data_ptr(), o.numel() * o.element_size()
-        for m, i in inputs.items():
-            b = i.data_ptr()
-            if a < b + i.numel() * i.element_size() and b < a + size:
+        if o is None:
+            continue
+        a, e = _span(o)
+        for m, b, f in spans:
+            if a < f and b < e:
                 raise ValueError(f"{n} overlaps {m}, which is read after it is written")
 
 
@@ -291,8 +300,9 @@ def build_page_tables(query_lens: torch.Tensor, context_lens: torch.Tensor, bloc
                            ("shortage", out.shortage, 1)):
             _need(t, "out." + name, torch.int32, (n,), dense=True)
             _on(device, **{"out." + name: t})
-        _apart(dict(query_lens=query_lens, context_lens=context_lens, block_table=block_table, free_pages=free_pages,
-                    free_head=free_head),
+        ins = dict(query_lens=query_lens, context_lens=context_lens, block_table=block_table, free_pages=free_pages,
+                   free_head=free_head)
+        _apart({n: t for n, t in ins.items() if t.is_contiguous()},   # others are copied first
                {"out." + n: t for n, t in zip(out._fields, out) if n != "free_head"})
     _need_gpu(device)
     sizes = [N + 1, N, max_tokens, max_tokens, 1]

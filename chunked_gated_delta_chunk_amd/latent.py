@@ -10,7 +10,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import ops
-from .blocks import _launch, _need_gpu, _on, _ptr
+from .blocks import _apart, _launch, _need_gpu, _on, _ptr
 from .ops import CDR_OK, _need, _raise, load_library
 
 LATENT_DIM, LATENT_ROPE = 512, 64
@@ -130,8 +130,8 @@ def latent_decode_fwd(q_latent: torch.Tensor, q_rope: torch.Tensor, cache: torch
     Returns ``(o, lse)``: o ``[.., H, 512]`` bf16 (the weighted latents, before the value
     up-projection) and the log of the sum of exponentials ``[.., H]`` fp32; rows that no packed
     sequence holds are zeros and -inf.  ``out``, ``lse_out`` and ``workspace`` (uint8,
-    :func:`latent_decode_workspace_bytes`) optionally supply the buffers; in the former two such rows
-    are left as they were.
+    :func:`latent_decode_workspace_bytes`) optionally supply the buffers, apart from the inputs; in the
+    former two such rows are left as they were.
     """
     lib = load_library()
     if not isinstance(q_latent, torch.Tensor) or q_latent.dim() != 4 or q_latent.shape[3] != LATENT_DIM:
@@ -171,6 +171,9 @@ def latent_decode_fwd(q_latent: torch.Tensor, q_rope: torch.Tensor, cache: torch
     st = lib.cdr_latent_decode_check(ref)
     if st != CDR_OK:
         _raise(st, "latent_decode_fwd")
+    if out is not None or lse_out is not None:
+        _apart(dict(q_latent=qc, q_rope=qr, cache=cache, block_table=block_table, seq_lens=seq_lens, cu_seqlens=cu_seqlens),
+               dict(out=out, lse_out=lse_out))
     _need_gpu(device)
     need = lib.cdr_latent_decode_workspace_bytes(ref)
     if workspace is None:
@@ -179,9 +182,9 @@ def latent_decode_fwd(q_latent: torch.Tensor, q_rope: torch.Tensor, cache: torch
         raise ValueError("workspace too small")
     elif not workspace.is_contiguous() or workspace.data_ptr() % 16:
         raise ValueError("workspace must be contiguous and 16-byte aligned")
-    out, lse_out = _results(p, out, lse_out, (B, T, H, LATENT_DIM), device)
     block_table, seq_lens = block_table.contiguous(), seq_lens.contiguous()
     cu = None if cu_seqlens is None else cu_seqlens.contiguous()
+    out, lse_out = _results(p, out, lse_out, (B, T, H, LATENT_DIM), device)
     _launch(device, "latent_decode_fwd", lib.cdr_latent_decode_fwd, ref, _ptr(qc), _ptr(qr), _ptr(cache),
             _ptr(block_table), _ptr(seq_lens), _ptr(cu), _ptr(out), _ptr(lse_out), _ptr(workspace),
             workspace.numel() * workspace.element_size())
@@ -258,8 +261,8 @@ def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor,
     zeros and -inf.  Packed batches have B = 1, ``cu_seqlens`` int32 ``[N+1]`` for the queries and
     ``cu_seqlens_k`` for the keys (the same when None).  ``scale=None`` means ``192 ** -0.5``; it must
     be positive.  Returns ``(o, lse)``: ``[B,T,H,128]`` bf16 and ``[B,T,H]`` fp32; rows that no packed
-    sequence holds are zeros and -inf.  ``out`` and ``lse_out`` optionally supply the buffers; in them
-    such rows are left as they were.
+    sequence holds are zeros and -inf.  ``out`` and ``lse_out`` optionally supply the buffers, apart from
+    the inputs; in them such rows are left as they were.
     """
     c = _LatentAttn(q, k_nope, k_rope, v, scale, cu_seqlens, cu_seqlens_k, "latent_attn_fwd")
     if out is not None:
@@ -269,6 +272,9 @@ def latent_attn_fwd(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor,
     if lse_out is not None:
         _need(lse_out, "lse_out", torch.float32, (c.B, c.T, c.H), dense=True)
     _on(c.device, out=out, lse_out=lse_out)
+    if out is not None or lse_out is not None:
+        _apart(dict(zip(("q", "k_nope", "k_rope", "v", "cu_seqlens", "cu_seqlens_k"), c.tensors)),
+               dict(out=out, lse_out=lse_out))
     _need_gpu(c.device)
     out, lse_out = _results(c.p, out, lse_out, (c.B, c.T, c.H, VALUE_DIM), c.device)
     _launch(c.device, "latent_attn_fwd", c.lib.cdr_latent_attn_fwd, ctypes.byref(c.p), *c.inputs, _ptr(out),

@@ -239,6 +239,35 @@ def test_latent_decode_binding_errors():
             cdr.latent_cache_write(*args)
 
 
+def test_latent_outputs_over_inputs_are_refused():
+    """An output that lies over an input, whole or in part, also over a strided one; neighbours are none."""
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    T, H = 6, 2
+    q, kr = b(1, T, H, 192), b(1, T, 64)
+    buf = b(4 * T * H * 128)
+    part = lambda at: buf[at * T * H * 128 // 2:][:T * H * 128].view(1, T, H, 128)  # noqa: E731
+    v, k = part(0), b(1, T, H, 128)
+    kv = buf[:2 * T * H * 128].view(1, T, H, 256)
+    lse = torch.zeros(1, T, H)
+    for kw in (dict(v=v, out=v), dict(v=v, out=part(1)), dict(k_nope=part(2), out=part(2)),
+               dict(k_nope=kv[..., :128], v=kv[..., 128:], out=part(1)), dict(k_nope=kv[..., :128], out=part(3)),
+               dict(lse_out=kr.view(-1)[:2 * T * H].view(torch.float32).view(1, T, H))):
+        with pytest.raises(ValueError, match="overlaps"):
+            cdr.latent_attn_fwd(**{**dict(q=q, k_nope=k, k_rope=kr, v=b(1, T, H, 128)), **kw})
+    with pytest.raises(ValueError, match="GPU"):      # apart: refused for nothing else than the device
+        cdr.latent_attn_fwd(q, k, kr, v, out=part(2), lse_out=lse)
+    with pytest.raises(ValueError, match="GPU"):
+        cdr.latent_attn_fwd(q, kv[..., :128], kr, kv[..., 128:], out=part(4))
+    ql = b(2, 1, 4, 512)
+    good = dict(q_latent=ql, q_rope=b(2, 1, 4, 64), cache=b(3, 16, 576), block_table=i(2, 2), seq_lens=i(2), scale=0.1)
+    for kw in (dict(out=ql), dict(out=good["cache"].view(-1)[576:][:4096].view(2, 1, 4, 512))):
+        with pytest.raises(ValueError, match="overlaps"):
+            cdr.latent_decode_fwd(**{**good, **kw})
+    with pytest.raises(ValueError, match="GPU"):
+        cdr.latent_decode_fwd(**good, out=b(2, 1, 4, 512))
+
+
 def test_latent_attention_oracle_gradients_match_differences():
     from oracle import latent
     g = torch.Generator().manual_seed(2)
