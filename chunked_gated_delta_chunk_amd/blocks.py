@@ -265,7 +265,9 @@ def build_page_tables(query_lens: torch.Tensor, context_lens: torch.Tensor, bloc
     cached; ``block_table`` int32 ``[N, W]``, updated in place with the new pages, which are taken
     from ``free_pages`` int32 ``[F]`` at ``free_head`` int32 ``[1]``.  ``free_head`` is advanced in
     place unless ``free_head_out`` is given.  ``max_tokens`` is the size of the token arrays (a
-    captured step's): positions and slots behind the last request are 0 and -1.  Nothing is read
+    captured step's): positions and slots behind the last request are 0 and -1.  ``cu_seqlens`` then ends
+    below ``max_tokens``, which latent attention takes as it is; :func:`chunk_dr_fwd` and
+    :func:`fused_recurrent_fwd` need offsets that end at their T.  Nothing is read
     back to the host; ``shortage`` says how many pages were missing.  ``out`` reuses the tensors of
     an earlier call, as a captured graph does (``free_head`` of it is ignored); they must not overlap
     the inputs, so an earlier call's ``seq_lens`` taken as ``context_lens`` is not also this call's.

@@ -485,9 +485,11 @@ cdr_status cdr_block_norm_bwd(const cdr_block_norm_problem* p, const void* y, co
                               void* stream);
 
 /* ------------------------------------------------------------------------------------------
- * Bookkeeping of a serving step on the device, from the lengths of its requests: the offsets that
- * the packed forward and decode take (cu_seqlens), positions, the page table and the slots of a
- * paged cache, with new pages taken from a list of free ones.  All arrays are int32 on the device;
+ * Bookkeeping of a serving step on the device, from the lengths of its requests: the offsets of its
+ * packed tokens (cu_seqlens), positions, the page table and the slots of a paged cache, with new pages
+ * taken from a list of free ones.  Latent attention takes the offsets as they are, also in a step padded
+ * to a captured size, where cu_seqlens[N] < max_tokens; the chunked and the per-token forward of the delta
+ * rule need offsets that end at their T, so there max_tokens is the step's own number of tokens.  All arrays are int32 on the device;
  * with q_n = max(query_lens[n], 0), c_n = max(context_lens[n], 0), P = page_size, W = table_cols:
  *
  *     cu_seqlens[0] = 0, cu_seqlens[n + 1] = min(cu_seqlens[n] + q_n, max_tokens)
