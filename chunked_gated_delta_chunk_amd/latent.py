@@ -75,7 +75,8 @@ def latent_cache_write(c: torch.Tensor, k_rope: torch.Tensor, cache: torch.Tenso
     ``c [..., 512]`` and ``k_rope [..., 64]`` bf16 of T tokens in all; ``cache [P, page, 576]`` bf16;
     ``slot_map`` int32 of T slots (:func:`build_page_tables` makes it): token t becomes row
     ``slot_map[t]`` of the cache's ``P * page`` rows, and slots outside them are skipped.  Two tokens
-    with one slot give an undefined row.
+    with one slot give an undefined row.  c and k_rope may be rows of the cache itself, to copy pages,
+    where no slot names one of them.
     """
     lib = load_library()
     if c.dim() < 1 or k_rope.dim() < 1 or c.shape[-1] != LATENT_DIM or k_rope.shape[-1] != LATENT_ROPE:

@@ -50,7 +50,7 @@
 extern "C" {
 #endif
 
-#define CDR_VERSION 9
+#define CDR_VERSION 10
 
 typedef enum {
     CDR_OK = 0,
@@ -594,7 +594,8 @@ cdr_status cdr_latent_decode_fwd(const cdr_latent_decode_problem* p, const void*
 /*
  * Writes T tokens' latents into the cache: row slot_map[t] of cache [num_pages * page_size, 576]
  * becomes (c[t], k_rope[t]).  Slots outside the cache are skipped (padding, as
- * cdr_build_page_tables marks it with -1); two tokens with one slot give an undefined row.
+ * cdr_build_page_tables marks it with -1); two tokens with one slot give an undefined row.  c and k_rope
+ * may be rows of the cache itself where no slot names one of them.
  *   c bf16 [T, 512], k_rope bf16 [T, 64]: token strides in elements, multiples of 8; c, k_rope
  *   and cache 16-byte aligned; slot_map int32 [T]
  */

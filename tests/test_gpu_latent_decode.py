@@ -303,6 +303,18 @@ def test_cache_write():
         assert torch.equal(got.cpu().view(320, 576), want)
 
 
+def test_cache_write_from_the_cache_itself():
+    """Pages copied to others, as for a request that takes over another's beginning."""
+    cache = torch.randn(9, 8, 576, generator=torch.Generator().manual_seed(21)).to(BF16).to(DEV)
+    want = cache.clone()
+    want[6:9] = cache[1:4]
+    want[0, 3] = cache[4, 7]
+    cdr.latent_cache_write(cache[1:4, :, :512], cache[1:4, :, 512:], cache,
+                           torch.arange(48, 72, dtype=torch.int32, device=DEV))
+    cdr.latent_cache_write(cache[4, 7:, :512], cache[4, 7:, 512:], cache, torch.tensor([3], dtype=torch.int32, device=DEV))
+    assert torch.equal(cache, want)
+
+
 def test_a_serving_step():
     """Three decode steps from request lengths: page tables, cache write, attention, all on the GPU,
     against attention over the plain history."""
