@@ -107,10 +107,9 @@ __device__ __forceinline__ bool attn_slot(const LatentAttnArgs& a, const int32_t
 }
 
 // The same with the heaviest blocks first, `rank` counting them: of up to 64 packed sequences, all last blocks
-// of the longest, then those a block shorter and so on (FIRST: all first blocks, then all second ones).  With
-// few blocks for each CU the device otherwise ends with a long sequence's heavy blocks alone: 5 sequences of
-// 8168 tokens, 16 heads, 129 us in the slots' order and 121 us in this one.
-template <int ROWS, bool FIRST>
+// of the longest, then those a block shorter and so on.  With few blocks for each CU the device otherwise ends
+// with a long sequence's heavy blocks alone.
+template <int ROWS>
 __device__ __forceinline__ bool attn_ranked(const LatentAttnArgs& a, const int32_t* cu, int T, int rank, int& n, int& block) {
     const int lane = threadIdx.x & 63;
     int blocks = 0;
@@ -122,8 +121,7 @@ __device__ __forceinline__ bool attn_ranked(const LatentAttnArgs& a, const int32
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) most = max(most, __shfl_xor(most, m, 64));
     most = __builtin_amdgcn_readfirstlane(most);
-    for (int i = 0; i < most; ++i) {
-        const int b = FIRST ? i : most - 1 - i;
+    for (int b = most - 1; b >= 0; --b) {
         uint64_t with = __ballot(blocks > b);
         const int count = __popcll(with);
         if (rank < count) {
@@ -137,11 +135,11 @@ __device__ __forceinline__ bool attn_ranked(const LatentAttnArgs& a, const int32
     return false;
 }
 
-// The block of a workgroup: heaviest first.
-template <int ROWS, bool FIRST>
-__device__ __forceinline__ bool attn_block(const LatentAttnArgs& a, const int32_t* cu, int T, int i, int& n, int& block) {
-    if (a.ranked) return attn_ranked<ROWS, FIRST>(a, cu, T, i, n, block);
-    return attn_slot<ROWS>(a, cu, T, FIRST ? i : a.slots - 1 - i, n, block);
+// The block of rows of a workgroup: heaviest first.
+template <int ROWS>
+__device__ __forceinline__ bool attn_block(const LatentAttnArgs& a, int i, int& n, int& block) {
+    if (a.ranked) return attn_ranked<ROWS>(a, a.cuq, a.T, i, n, block);
+    return attn_slot<ROWS>(a, a.cuq, a.T, a.slots - 1 - i, n, block);
 }
 
 // Copies rows `first` .. + 63 (clipped to `last`) of an array with 256-byte or 128-byte rows to LDS:
@@ -255,7 +253,7 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     }
     const int h = blockIdx.x % a.H;
     int n, block;
-    if (!attn_block<A_ROWS, false>(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;
+    if (!attn_block<A_ROWS>(a, blockIdx.x / a.H, n, block)) return;
     const Seq s = attn_seq(a, n);
     const Tiles at = {lds_offset(kn), lds_offset(kr), lds_offset(vt)};
     const Reads reads(lane);
@@ -391,7 +389,7 @@ __global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kerne
         fill_unheld(reinterpret_cast<uint4*>(a.o), a.H * (AQ / 8), make_uint4(0, 0, 0, 0), a.cuq, a.N, a.T, blockIdx.x, gridDim.x);
     const int h = blockIdx.x % a.H;
     int n, block;
-    if (!attn_block<ROWS, false>(a, a.cuq, a.T, blockIdx.x / a.H, n, block)) return;
+    if (!attn_block<ROWS>(a, blockIdx.x / a.H, n, block)) return;
     const Seq s = attn_seq(a, n);
     char* kn = lds;
     char* kr = kn + 2 * A_TILE * 256;
@@ -543,7 +541,7 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = blockIdx.x % a.H;
     int n, block;
-    if (!attn_block<A_ROWS, true>(a, a.cuk, a.Tk, blockIdx.x / a.H, n, block)) return;
+    if (!attn_slot<A_ROWS>(a, a.cuk, a.Tk, blockIdx.x / a.H, n, block)) return;
     const Seq s = attn_seq(a, n);
     const Reads reads(lane);
     const int key = block * A_ROWS + 32 * w + (lane & 31);
@@ -794,12 +792,22 @@ int64_t attn_slots(int64_t T, const cdr_latent_attn_problem* p, int rows = A_ROW
     return p->varlen ? T / rows + p->N : p->N * ((T + rows - 1) / rows);
 }
 
-// Slots of a launch, and whether its blocks are taken by weight: of 2 to 64 packed sequences with at most
-// sixteen blocks a CU.  With more the last ones are a small part, and finding a block costs steps in the
-// number of blocks a sequence has.
-void set_order(LatentAttnArgs& a, const cdr_latent_attn_problem* p, int64_t slots) {
-    a.slots = (int)slots;
-    a.ranked = p->varlen && p->N >= 2 && p->N <= 64 && slots * p->H <= 16 * A_CUS;
+// Slots of a launch over rows, and whether its blocks are taken by weight: of 2 to `most` packed sequences with at
+// most six blocks of 128 rows a CU.  Ragged batches of 16 heads, time by weight over time by slot, forward and dq:
+//
+//     sequences        2             5             8             16            32            48            64
+//     4000 tokens   1.00  0.93    0.92  0.90    0.93  0.91    0.87  0.94    1.09  0.90    1.09  0.97    1.15  0.97
+//     8168          0.97  0.98    0.87  0.86    0.80  0.88    0.88  0.93    0.99  0.88    1.00  0.99    1.04  0.90
+//     12000         0.96  0.93    0.89  0.99    0.90  0.97    0.92  0.92    1.01  0.88    1.02  0.91    1.08  0.94
+//     16000         1.01  1.03    1.00  1.07    0.92  0.96    0.97  0.98                                1.08  1.01
+//     16000, 32 heads  1.03 1.05  1.02  1.05    1.02  1.05    1.04  1.05                                1.16  1.03
+//
+// (8168 tokens of 5 sequences: 119 and 104 us, 197 and 170.)  Finding a block costs steps in the number of blocks a
+// sequence has, and in short forwards of many sequences that shows: they stop at 32, dq at 64.  dk and dv go by slot:
+// by weight they took longer in 35 of 40 such batches, 7 % in the middle and 29 % at most.
+void set_order(LatentAttnArgs& a, const cdr_latent_attn_problem* p, int rows, int most) {
+    a.slots = (int)attn_slots(p->T, p, rows);
+    a.ranked = p->varlen && p->N >= 2 && p->N <= most && attn_slots(p->T, p) * p->H <= 6 * A_CUS;
 }
 
 bool ok_stride(int64_t s) { return s >= 0 && (s & 7) == 0 && s < (1 << 23); }
@@ -862,7 +870,7 @@ cdr_status cdr_latent_attn_fwd(const cdr_latent_attn_problem* p, const void* q, 
     cdr::LatentAttnArgs a = cdr::attn_args(p, q, k_nope, k_rope, v, cu_seqlens, cu_seqlens_k);
     a.o = static_cast<uint16_t*>(o);
     a.lse = lse;
-    cdr::set_order(a, p, cdr::attn_slots(p->T, p));
+    cdr::set_order(a, p, cdr::A_ROWS, 32);
     hipLaunchKernelGGL(cdr::latent_fwd_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0,
                        static_cast<hipStream_t>(stream), a);
     return hipGetLastError() == hipSuccess ? CDR_OK : CDR_ERR_HIP;
@@ -900,15 +908,14 @@ cdr_status cdr_latent_attn_bwd(const cdr_latent_attn_problem* p, const void* q, 
     if (tq > 0) {
         const uint16_t* fo = static_cast<const uint16_t*>(o);
         const bool large = cdr::attn_slots(p->T, p, 256) * p->H >= 2 * cdr::A_CUS;
-        cdr::set_order(a, p, cdr::attn_slots(p->T, p, large ? 256 : 128));
+        cdr::set_order(a, p, large ? 256 : 128, 64);
         const dim3 grid((unsigned)(a.slots * (int64_t)a.H));
         if (large) hipLaunchKernelGGL((cdr::latent_dq_kernel<256>), grid, dim3(512), 0, s, a, fo);
         else hipLaunchKernelGGL((cdr::latent_dq_kernel<128>), grid, dim3(256), 0, s, a, fo);
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
     }
     if (tk > 0) {
-        cdr::set_order(a, p, cdr::attn_slots(p->Tk, p));
-        hipLaunchKernelGGL(cdr::latent_dkv_kernel, dim3((unsigned)(a.slots * (int64_t)a.H)), dim3(256), 0, s, a);
+        hipLaunchKernelGGL(cdr::latent_dkv_kernel, dim3((unsigned)(cdr::attn_slots(p->Tk, p) * p->H)), dim3(256), 0, s, a);
         if (hipGetLastError() != hipSuccess) return CDR_ERR_HIP;
         hipLaunchKernelGGL(cdr::latent_dkr_kernel, dim3((unsigned)((tk * (cdr::LR / 4) + 255) / 256)), dim3(256), 0, s, a.dkr,
                            static_cast<uint16_t*>(dk_rope), a.cuk, p->N, (int)tk, p->H, a.fill);

@@ -270,6 +270,19 @@ def test_many_short_sequences_in_either_order(n):
     run(*make(lens, [x + (i % 3) * 50 for i, x in enumerate(lens)], 1, 50 + n))
 
 
+@pytest.mark.parametrize("n,H", [(32, 2), (33, 2), (5, 76), (5, 77)])
+def test_orders_of_the_forward(n, H):
+    """The forward takes up to 32 packed sequences by weight, and up to 1536 blocks of 128 rows: 5 sequences of 2000
+    rows make 20 a head."""
+    g = torch.Generator().manual_seed(n + H)
+    if n == 5:
+        lens = [1100, 3, 400, 297, 200]
+    else:
+        lens = torch.randint(0, 60, (n,), generator=g).tolist()
+        lens[3] = 290
+    run(*make(lens, [x + (i % 2) * 9 for i, x in enumerate(lens)], H, 70 + n + H))
+
+
 def test_dq_in_blocks_of_either_size():
     """256 blocks of 256 rows and more take the larger blocks."""
     kw, do = make([257, 30, 513], [257, 30, 600], 64, 44)
