@@ -30,10 +30,10 @@
 // a second kernel joins in order.  The cut depends on the lengths and sizes alone, so the same inputs
 // give the same bits.
 //
-// Measured: 256 sequences of up to 8192 keys, 16 heads, 232 us, 5.3 TB/s of cache, which HBM bounds; 64
-// sequences of 4 tokens and 64 heads, up to 4096 keys, 140 us, of which the copies to LDS alone (four row
-// blocks read each key, 10 TB/s) take 74; 8192 keys of one sequence, 16 heads, 11.5 us and 7.3 for the
-// join, all latency.
+// Measured, inputs changing from call to call: 256 sequences of up to 8192 keys, 16 heads, 225 us, 5.4 TB/s of cache,
+// which HBM bounds; 64 sequences of 4 tokens and 64 heads, up to 4096 keys, 142 us, of which the copies to LDS alone
+// (four row blocks read each key, 10 TB/s) take 74; 8192 keys of one sequence, 16 heads, 13.6 us and 7.3 for the join,
+// all latency.
 #include "chunk_dr.h"
 #include "cdr_latent.h"
 
@@ -43,7 +43,9 @@ namespace {
 
 constexpr int DEC_GRID = 256;        // workgroups; LDS holds one on a CU
 constexpr int DEC_KEYS = 64;         // keys of a tile
-constexpr int DEC_TEAM = 8;          // most row blocks that are taken side by side
+// Most row blocks that are taken side by side.  64 sequences of 512 rows, up to 4096 keys, with 1, 2, 4, 8 and 16: 308,
+// 266, 259, 254 and 254 us; of 256 rows (four blocks) 168, 148, 147; 256 sequences of 2048 rows with 8 and 16: 1924, 1838.
+constexpr int DEC_TEAM = 8;
 // Keys of a sequence at most: pages are looked up two tiles ahead, up to key len + 190, which stays in int.
 constexpr int64_t DEC_MAX_LEN = (int64_t)INT32_MAX - 255;
 
@@ -607,10 +609,17 @@ __global__ __launch_bounds__(256) void latent_write_kernel(const uint16_t* c, co
         *reinterpret_cast<uint4*>(to + LC + 8 * lane) = *reinterpret_cast<const uint4*>(r + t * rs + 8 * lane);
 }
 
-// Rows of a block: the fewest of 16, 32 and 64 that hold the rows of a sequence (of an average one
-// in a packed batch); more rows would be computed for nothing, fewer would read the keys again.  64 sequences
-// of up to 4096 keys with blocks of 16, 32 and 64: 16 heads 56, 58 and 65 us, 32 heads 71, 66 and 70, 64
-// heads 109, 82 and 82, 128 heads 178, 106 and 108.
+// Rows of a block: the fewest of 16, 32 and 64 that hold the rows of a sequence (of an average one in a packed
+// batch, whose T counts spare tokens too); more rows would be computed for nothing, fewer would read the keys again.
+// Decode and join, us, with blocks of 16, 32 and 64:
+//
+//     rows a sequence                     16             32             64             128             256
+//     64 sequences, to 4096 keys      52  54  60     61  60  65     93  73  75     147 112  96     277 179 149
+//     256 sequences, to 2048 keys     92  97 106    120 112 117    192 140 142     352 221 183     642 402 303
+//     8 sequences, to 8192 keys       31  33  37     33  39  41     40  42  48      56  49  53      88  66  64
+//     1 sequence, 16384 keys          27  28  30     26  32  33     29  33  37      35  36  41      51  44  47
+//
+// (Few sequences would take blocks of half the size or less up to 64 rows, where the device is not full.)
 int dec_m(const cdr_latent_decode_problem* p) {
     const int64_t tokens = p->varlen ? ((int64_t)p->T + p->N - 1) / p->N : p->T;
     const int64_t rows = tokens * p->H;
@@ -690,7 +699,8 @@ cdr_status cdr_latent_decode_fwd(const cdr_latent_decode_problem* p, const void*
     a.num_pages = p->num_pages;
     a.shift = __builtin_ctz((unsigned)p->page_size);
     a.scale2 = p->scale * cdr::LOG2E;
-    // packed batches have row blocks of no common number: each is a unit of its own
+    // Packed batches have row blocks of no common number: each is a unit of its own, and a sequence's blocks read its
+    // keys one after the other (64 sequences of 256 rows, up to 4096 keys: 149 us as a batch, 171 us packed).
     const int64_t blocks = ((int64_t)p->T * p->H + m - 1) / m;
     a.team = p->varlen ? 1 : (int)(blocks < cdr::DEC_TEAM ? blocks : cdr::DEC_TEAM);
     hipStream_t s = static_cast<hipStream_t>(stream);

@@ -238,9 +238,11 @@ __device__ __forceinline__ void load_keys(const LatentAttnArgs& a, const Seq& s,
 // score.  Weights over 1 are as exact in bf16 and their sums in fp32; but the largest weight is 1 and exact where m
 // is its score, and so it stays for every key that carries a sixteenth of its row or more.
 //
-// 8192 tokens, 16 heads: 369 us, 0.93 PFLOP/s, the matrix unit 56 % busy; the softmax's arithmetic, which both
-// workgroups of a SIMD share, and the waits at its ends bound the rest.  (One call alone 352 us; with o rescaled at
-// every new maximum 380, and 373 so without the preference.)
+// 8192 tokens, 16 heads: 340 us, 1.01 PFLOP/s, the matrix unit 55 % busy; the softmax's arithmetic, which both
+// workgroups of a SIMD share, and the waits at its ends bound the rest.  The two go together, and pay in that range
+// of lengths: 8192 tokens 341 us with both, 364 without the preference, 371 with o rescaled at every new maximum, 363
+// with neither; 5 packed sequences of 8168 tokens 111, 111, 113 and 110; 2048 tokens 54.4, 52.2, 54.7 and 52.4; 32768
+// tokens 5.15, 5.23, 5.09 and 5.06 ms.
 __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
     __shared__ __align__(256) char lds[A_LDS];
     char* kn = lds;
@@ -377,10 +379,12 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
 // to bf16 would be a tenth of the error of dq and dk; behind many keys o is an average and its rounding counts
 // little.
 //
-// Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than two a CU, and a block's own
-// time is what counts (4 packed sequences with gradients, 8192 tokens: 16 heads 666 us with 128 and 615 with 256
-// rows, 8 heads 392 and 417; 1001 tokens of 8 heads 56 and 66).  8192 tokens, 16 heads: 573 us, the matrix unit
-// 55 % busy, 0.96 PFLOP/s with the scores that it computes again.
+// Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than two a CU (512), and a block's
+// own time is what counts.  Forward and gradients, us, with 128 and 256 rows: one sequence of 8192 tokens, 16 heads
+// (528 blocks of 256) 1717 and 1540, 8 heads (264) 924 and 976; 4 packed ones of 8192 tokens, 16 heads (576) 643 and
+// 589, 8 heads (288) 384 and 407; 2048 tokens, 64 heads (576) 547 and 499, 16 heads (144) 228 and 246; 1001 tokens of 7
+// sequences, 8 heads (80) 58 and 65; but 40 sequences of 8168 tokens, 8 heads (568) 158 and 163.  8192 tokens, 16 heads:
+// 503 us, the matrix unit 55 % busy, 1.09 PFLOP/s with the scores that it computes again.
 template <int ROWS>
 __global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kernel(LatentAttnArgs a, const uint16_t* o) {
     constexpr int NW = ROWS / 32;
@@ -523,7 +527,7 @@ __global__ __launch_bounds__(2 * ROWS, ROWS == 256 ? 2 : 1) void latent_dq_kerne
 
 // dk and dv of a block of 128 keys, and the head's part of dkr: one wave a SIMD, whose 512 registers hold v and
 // the 10 blocks of sums; the softmax of one half tile runs between the products of the other.  8192 tokens, 16
-// heads: 810 us, 0.85 PFLOP/s, the matrix unit 47 % busy: with one wave a SIMD, waits for LDS reads are not covered.
+// heads: 692 us, 0.99 PFLOP/s, the matrix unit 47 % busy: with one wave a SIMD, waits for LDS reads are not covered.
 __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
     __shared__ __align__(256) char lds[A_LDS];
     __shared__ __align__(256) char own[A_ROWS * (256 + 128)];   // this block's keys, 32 a wave: operands like v's,
@@ -772,7 +776,7 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(LatentAttnArgs a) {
         }
 }
 
-// dkr: the heads' parts added in order, 4 dimensions a thread.  8192 tokens, 16 heads: 7.5 us, 34 MB, mostly from
+// dkr: the heads' parts added in order, 4 dimensions a thread.  8192 tokens, 16 heads: 7.8 us, 34 MB, mostly from
 // the Infinity Cache.
 __global__ __launch_bounds__(256) void latent_dkr_kernel(const float* part, uint16_t* dkr, const int32_t* cuk, int N, int total,
                                                          int H, int fill) {
