@@ -20,8 +20,8 @@
 // elements each, 256 with 16 and 512 with 16: 35, 31 and 57, the gradients alone 90, 97 and 239.)  Beyond 4096
 // columns the backward's arrays do not all fit the registers: 92 to 180 of a lane's values wait in scratch
 // memory, and 2048 x 8192 take 177 us (1.5 TB/s) where 4096 x 4096 take 90 (3.0); forward 44 and 36.
-// 8192 x 2048 with an fp32 residual takes 48 us forward, 4.9 TB/s; with gradients, all bf16, 107
-// us, 4.1 TB/s, where the backward's three row sums are waited for.  Groups walk over rows with a fixed
+// 8192 x 2048 with an fp32 residual takes 48 us forward, 4.9 TB/s; with gradients, all bf16, 105
+// us, 4.2 TB/s, where the backward's three row sums are waited for.  Groups walk over rows with a fixed
 // stride, so the weights are loaded once and the backward's column sums stay in registers until the end,
 // where each workgroup writes one partial row; a second kernel adds the partial rows in a fixed order (no
 // atomics: the same inputs give the same bits).  Everything is computed in fp32; outputs are
