@@ -57,13 +57,13 @@ __device__ __forceinline__ bf16x8 lds16(const void* p) { return *static_cast<con
 // Packed rows that no sequence holds, in front of the first offset and behind the last one: each row's `units`
 // values of type T at base + row * units set to v.  The workgroups of a launch (`wg` of `wgs`) take rows in turn.
 template <typename T>
-__device__ __forceinline__ void fill_unheld(T* base, int units, const T& v, const int32_t* cu, int N, int total, int wg,
+__device__ __forceinline__ void fill_unheld(T* base, int64_t units, const T& v, const int32_t* cu, int N, int total, int wg,
                                             int wgs) {
     const int first = min(max(cu[0], 0), total), end = min(max(cu[N], first), total);
     const int64_t count = first + total - end;
     for (int64_t i = wg; i < count; i += wgs) {
-        T* p = base + (size_t)(i < first ? i : i - first + end) * units;
-        for (int u = threadIdx.x; u < units; u += blockDim.x) p[u] = v;
+        T* p = base + (i < first ? i : i - first + end) * units;
+        for (int64_t u = threadIdx.x; u < units; u += blockDim.x) p[u] = v;
     }
 }
 

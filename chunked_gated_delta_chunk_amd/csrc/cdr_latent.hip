@@ -264,7 +264,7 @@ __global__ __launch_bounds__(64 * NW, 1) void latent_decode_kernel(LatentDecodeA
     const int kg = w % KG, rh = w / KG;        // the wave's keys and row part in the scores
     const int wg = dec_wg();
     if (a.fill) {
-        fill_unheld(reinterpret_cast<uint4*>(a.o), a.H * (LC / 8), make_uint4(0, 0, 0, 0), a.cu, a.N, a.T, wg, DEC_GRID);
+        fill_unheld(reinterpret_cast<uint4*>(a.o), (int64_t)a.H * (LC / 8), make_uint4(0, 0, 0, 0), a.cu, a.N, a.T, wg, DEC_GRID);
         if (a.lse) fill_unheld(a.lse, a.H, -INFINITY, a.cu, a.N, a.T, wg, DEC_GRID);
     }
     Run run;

@@ -551,7 +551,7 @@ cdr_status cdr_build_page_tables(int32_t N, int32_t table_cols, int32_t num_free
  *              elements, multiples of 8; tokens = N * T, or T in all when varlen
  *   cache      bf16 [num_pages, page_size, 576], page_size a power of two
  *   block_table int32 [N, table_cols], seq_lens int32 [N], cu_seqlens int32 [N + 1] (varlen;
- *              offsets are clipped to [0, T])
+ *              offsets do not fall and are clipped to [0, T])
  *   o          bf16 [tokens, H, 512], lse fp32 [tokens, H] or NULL; rows that no sequence holds (in
  *              front of the first offset, behind the last) are left as they were, or become 0 and
  *              -inf with varlen CDR_VARLEN_FILL
@@ -620,8 +620,8 @@ cdr_status cdr_latent_cache_write(int32_t T, int32_t num_pages, int32_t page_siz
  *   k_nope   bf16 [keys, H, 128]                             strides (token, head)
  *   k_rope   bf16 [keys, 64]                                 stride of a token
  *   v        bf16 [keys, H, 128]                             strides (token, head)
- *   cu_seqlens, cu_seqlens_k  int32 [N + 1], varlen: rows' and keys' offsets, clipped to [0, T] and
- *            [0, Tk]; may be the same array.  Else every sequence has T rows and Tk keys.
+ *   cu_seqlens, cu_seqlens_k  int32 [N + 1], varlen: rows' and keys' offsets, which do not fall and are
+ *            clipped to [0, T] and [0, Tk]; may be the same array.  Else every sequence has T rows and Tk keys.
  *   o        bf16 [tokens, H, 128], lse fp32 [tokens, H]; dense.  Rows that no sequence holds (in front
  *            of the first offset, behind the last) are left as they were, or become 0 and -inf with
  *            varlen CDR_VARLEN_FILL.

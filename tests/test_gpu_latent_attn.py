@@ -367,6 +367,45 @@ def test_graph_replays():
             assert torch.equal(a, b)
 
 
+def test_padded_graph_replays():
+    """A captured step of 200 rows and 230 keys that holds fewer: what the last replay held and this one does not
+    is empty again."""
+    kw, do = make([150, 40], [170, 40], 2, 51, spare=10)
+    kw["k_rope"], kv = kw["k_rope"].new_zeros(1, 230, 64), torch.zeros(1, 230, 2, 256, dtype=BF16)
+    kw["k_nope"], kw["v"] = kv[..., :128], kv[..., 128:]
+    d, do = dev(kw), do.to(DEV)
+
+    def step():
+        o, lse = cdr.latent_attn_fwd(**d)
+        return (o, lse) + cdr.latent_attn_bwd(**d, o=o, lse=lse, do=do)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for seed, lq, lk in ((52, (150, 40), (170, 40)), (53, (3, 0), (9, 2)), (54, (0, 199), (10, 220)), (55, (0, 0), (0, 0))):
+        new, ndo = make(lq, lk, 2, seed)
+        for k, v in new.items():
+            if k.startswith("cu"):
+                d[k].copy_(v)
+            else:
+                d[k].fill_(math.nan)
+                d[k][:, :v.shape[1]] = v.to(DEV)
+        do.fill_(math.nan)
+        do[:, :sum(lq)] = ndo.to(DEV)
+        graph.replay()
+        torch.cuda.synchronize()
+        cut = lambda t, n: t[:, :n]  # noqa: E731
+        a, b = sum(lq), sum(lk)
+        compare(new, ndo, cut(held[0], a), cut(held[1], a), (cut(held[2], a),) + tuple(cut(t, b) for t in held[3:]),
+                192 ** -0.5)
+        for t, n, empty in zip(held, (a, a, a, b, b, b), (0, -math.inf, 0, 0, 0, 0)):
+            assert (t[:, n:] == empty).all()
+        for x, y in zip(held, step()):
+            assert torch.equal(x, y)
+
+
 def test_gradients_match_differences():
     """Directional differences of the forward itself: o's change along the gradient's direction, in the
     fp64 oracle's step, against the gradient's product with it."""
