@@ -376,8 +376,10 @@ __global__ __launch_bounds__(256, 2) void latent_fwd_kernel(LatentAttnArgs a) {
 //
 // delta is do . o from the forward's o, but for rows that see at most 128 keys it is summed from the weights.
 // There ds is a difference of two numbers of one size (a row of one key has ds = 0), o is large and its rounding
-// to bf16 would be a tenth of the error of dq and dk; behind many keys o is an average and its rounding counts
-// little.
+// to bf16 would be a tenth of the error of dq and dk; behind many keys that share a row o is an average and its
+// rounding counts little.  Where one key carries such a row it counts: the error of dq and dk, of which 1.7e-3 is
+// their own rounding, is 2.4e-3 with largest weights of 0.03 on average (2048 keys), 2.8e-3 with 0.29, 5.0e-3 with
+// 0.77 and 6.6e-3 with 0.92.
 //
 // Blocks of 256 rows, two waves a SIMD; of 128 where the 256-row ones are fewer than two a CU (512), and a block's
 // own time is what counts.  Forward and gradients, us, with 128 and 256 rows: one sequence of 8192 tokens, 16 heads
